@@ -1,0 +1,631 @@
+// AdamW over many tensors in one launch, its states in 32 or in 8 bits, and the
+// global gradient norm with the clip factor: the step of the parameters that
+// Muon does not take (embeddings, heads, norms, biases).
+//
+// Per element, with t the completed steps plus one and c the clip factor:
+//   g <- c g,  m <- b1 m + (1 - b1) g,  v <- b2 v + (1 - b2) g^2,
+//   p <- (1 - lr wd) p - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps).
+//
+// Everything here is bound by HBM: 28 B per element with fp32 states and an fp32
+// gradient, 14.1 B with 8-bit states and a 16-bit gradient. One pass moves each
+// byte once; the tensor table travels in the kernel's parameters, so a list of any
+// addresses needs no copy to the device and can be captured into a graph.
+
+#include <math.h>
+
+#include "gm_common.cuh"
+#include "gm_internal.h"
+
+namespace gm {
+namespace {
+
+constexpr int kGroup8 = 128;      // elements per scale of an 8-bit state
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// ------------------------------------------------------------ work distribution
+// The list is cut into chunks of kChunk elements of one tensor; first[i] is the
+// first chunk of tensor i. A CTA walks chunks blockIdx.x, + gridDim.x, ...
+template <int N>
+struct ChunkMap {
+  int count;
+  int first[N + 1];
+  __device__ __forceinline__ int total() const { return first[count]; }
+  // The tensor of a chunk at or after tensor i's first chunk.
+  __device__ __forceinline__ int find(int chunk, int i) const {
+    if (chunk < first[i + 1]) return i;
+    int lo = i + 1, hi = count - 1;   // first[lo] <= chunk < first[hi + 1]
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= chunk) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  }
+};
+
+// ------------------------------------------------------------------ load / store
+// Four consecutive elements from i on, `n` of them inside the tensor (n <= 0:
+// none). `vec`: the array is aligned for one vector access and n >= 4.
+template <int DT>
+__device__ __forceinline__ float one(const void* p, long long i) {
+  if constexpr (DT == GM_F32) return static_cast<const float*>(p)[i];
+  else return h16_to_float(static_cast<const uint16_t*>(p)[i], DT == GM_F16);
+}
+template <int DT>
+__device__ __forceinline__ void load4(const void* p, long long i, long long n, bool vec, float (&o)[4]) {
+  if (vec) {
+    if constexpr (DT == GM_F32) {
+      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+      o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+      o[0] = h16_to_float((uint16_t)(v.x & 0xFFFFu), DT == GM_F16);
+      o[1] = h16_to_float((uint16_t)(v.x >> 16), DT == GM_F16);
+      o[2] = h16_to_float((uint16_t)(v.y & 0xFFFFu), DT == GM_F16);
+      o[3] = h16_to_float((uint16_t)(v.y >> 16), DT == GM_F16);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = e < n ? one<DT>(p, i + e) : 0.f;
+  }
+}
+__device__ __forceinline__ void store4(void* p, long long i, long long n, bool vec, int dt,
+                                       const float (&v)[4]) {
+  if (vec) {
+    store4_from_float(p, i, dt, make_float4(v[0], v[1], v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) store_from_float(p, i + e, dt, v[e]);
+  }
+}
+__device__ __forceinline__ uint32_t load4_codes(const uint8_t* p, long long i, long long n, bool vec) {
+  if (vec) return *reinterpret_cast<const uint32_t*>(p + i);
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < n) w |= (uint32_t)p[i + e] << (8 * e);
+  return w;
+}
+__device__ __forceinline__ void store4_codes(uint8_t* p, long long i, long long n, bool vec, uint32_t w) {
+  if (vec) {
+    *reinterpret_cast<uint32_t*>(p + i) = w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) p[i + e] = (uint8_t)(w >> (8 * e));
+  }
+}
+
+// ------------------------------------------------------------------ 8-bit states
+// m: e4m3 codes under sm = max(max|m| / 448, 2^-126). v: its root r under
+// sv = max(max r / 1.9375, 2^-126), as a float of four exponent and four mantissa
+// bits without a sign (2^-18 to 1.9375; r spans v's range at half its exponents,
+// and half a step is 3 % of r). A v that fp32 holds as non-zero keeps code 1 at
+// least, so that no denominator falls to eps while m lives. The floor 2^-126
+// keeps 1 / scale finite.
+constexpr float kScaleFloor = 1.17549435e-38f;   // 2^-126
+constexpr float kTopM = 448.0f, kTopR = 1.9375f;
+
+__device__ __forceinline__ float scale_of(float top, float inv_max) {
+  // a group with an infinity or a NaN is NaN as a whole
+  return top <= 3.402823466e38f ? fmaxf(__fmul_rn(top, inv_max), kScaleFloor) : __int_as_float(0x7fffffff);
+}
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ void e4m3x4_to_float(uint32_t w, float (&o)[4]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)(w >> (16 * h))));
+    o[2 * h] = __half2float(__ushort_as_half((uint16_t)(d & 0xFFFFu)));
+    o[2 * h + 1] = __half2float(__ushort_as_half((uint16_t)(d >> 16)));
+  }
+}
+// Exponents 0..15 of the 4 + 4 bit float are fp32's own lowest ones (a value x is
+// kept as the fp32 number x 2^-112): code << 19 are that number's bits, subnormals
+// included, and rounding to nearest even is on the bits.
+__device__ __forceinline__ float root_value(uint32_t code) {
+  return __fmul_rn(__uint_as_float(code << 19), 5.192296858534828e33f);   // 2^112
+}
+__device__ __forceinline__ uint32_t root_bits(float y) {
+  return __float_as_uint(__fmul_rn(y, 1.925929944387236e-34f));           // 2^-112
+}
+__device__ __forceinline__ uint32_t root_code(uint32_t bits, float v) {
+  const uint32_t c = min((bits + 0x3FFFFu + ((bits >> 19) & 1u)) >> 19, 255u);
+  return v > 0.f ? max(c, 1u) : c;
+}
+
+// Both codes from fp64 values (round to nearest, ties to even).
+__device__ __forceinline__ double pow2d(int e) { return __hiloint2double((e + 1023) << 20, 0); }
+__device__ __forceinline__ uint32_t e4m3_from_double(double y) {
+  const double a = fmin(fabs(y), 448.0);
+  const int e = max((__double2hiint(a) >> 20) - 1023, -6);
+  const int k = (int)rint(a * pow2d(3 - e));
+  return (uint32_t)(((e + 6) << 3) + k) | (y < 0.0 ? 0x80u : 0u);
+}
+__device__ __forceinline__ uint32_t root_from_double(double y, double v) {
+  const int e = max((__double2hiint(y) >> 20) - 1023, -14);
+  const int k = (int)rint(fmin(y, 2.0) * pow2d(4 - e));
+  const uint32_t c = min((uint32_t)(((e + 14) << 4) + k), 255u);
+  return (float)v > 0.f ? max(c, 1u) : c;
+}
+
+__device__ __forceinline__ double warp_max(double x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = fmax(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+// --------------------------------------------------------------------- the step
+// What every chunk of a step needs, computed once per step by k_adamw_begin.
+struct Coef {
+  double c;          // clip factor (1 without)
+  float c32;
+  float decay;       // 1 - lr wd
+  float scale;       // lr / (1 - b1^t)
+  float root;        // 1 / sqrt(1 - b2^t)
+  int skip;
+};
+static_assert(sizeof(Coef) <= GM_ADAMW_SCRATCH_BYTES, "the step's scratch holds the coefficients");
+
+__global__ void k_adamw_begin(double lr, double b1, double b2, double wd, const double* clip,
+                              const float* lr_dev, const int32_t* skip, int64_t* step, Coef* out) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (skip && *skip) {
+    out->skip = 1;
+    return;
+  }
+  const long long t = *step + 1;
+  *step = t;
+  const double l = lr_dev ? (double)*lr_dev : lr;
+  const double c = clip ? *clip : 1.0;
+  out->c = c;
+  out->c32 = (float)c;
+  out->decay = (float)(1.0 - l * wd);
+  out->scale = (float)(l / (1.0 - pow(b1, (double)t)));
+  out->root = (float)(1.0 / sqrt(1.0 - pow(b2, (double)t)));
+  out->skip = 0;
+}
+
+struct Entry {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* mscale;
+  float* vscale;
+  void* copy;
+  long long numel;
+};
+constexpr int kMaxTensors = 440;   // per launch: a table of 30.4 KB of the 32 KB of parameters
+struct Table {
+  ChunkMap<kMaxTensors> map;
+  uint8_t vec[kMaxTensors];
+  Entry e[kMaxTensors];
+};
+struct Consts {
+  float b1, ob1, b2, ob2, eps;   // ob = 1 - b, rounded once from fp64
+  double db1, dob1, db2, dob2;
+  int cdt;
+};
+
+constexpr int kUnroll = 2;                                    // groups of a warp in flight
+constexpr int kChunk = kWarps * kUnroll * kGroup8;
+
+template <int PDT, int GDT, int BITS>
+__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Table t, const Consts k,
+                                                    const Coef* __restrict__ coef) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (coef->skip) return;
+  const float c = coef->c32, decay = coef->decay, scale = coef->scale, root = coef->root;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int ti = 0;
+  for (int chunk = blockIdx.x; chunk < t.map.total(); chunk += gridDim.x) {
+    ti = t.map.find(chunk, ti);
+    const Entry& E = t.e[ti];
+    const long long base = (long long)(chunk - t.map.first[ti]) * kChunk + warp * (kUnroll * kGroup8);
+    const long long left = E.numel - base;   // of this warp's part
+    if (left <= 0) continue;
+    float p[kUnroll][4], g[kUnroll][4], m[kUnroll][4], v[kUnroll][4];
+    uint32_t mc[kUnroll], vc[kUnroll];
+    float ms[kUnroll], vs[kUnroll];
+    const bool aligned = t.vec[ti] != 0;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const long long i = base + u * kGroup8 + lane * 4, n = E.numel - i;
+      const bool vec = aligned && n >= 4;
+      load4<PDT>(E.p, i, n, vec, p[u]);
+      load4<GDT>(E.g, i, n, vec, g[u]);
+      if constexpr (BITS == 32) {
+        load4<GM_F32>(E.m, i, n, vec, m[u]);
+        load4<GM_F32>(E.v, i, n, vec, v[u]);
+      } else {
+        mc[u] = load4_codes(static_cast<const uint8_t*>(E.m), i, n, vec);
+        vc[u] = load4_codes(static_cast<const uint8_t*>(E.v), i, n, vec);
+        const bool in = left > u * kGroup8;
+        const long long grp = base / kGroup8 + u;
+        ms[u] = in ? E.mscale[grp] : 0.f;
+        vs[u] = in ? E.vscale[grp] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const long long i = base + u * kGroup8 + lane * 4, n = E.numel - i;
+      const bool vec = aligned && n >= 4;
+      float mo[4], ro[4];          // decoded m and r (8-bit states)
+      if constexpr (BITS == 8) {
+        e4m3x4_to_float(mc[u], mo);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          m[u][e] = __fmul_rn(mo[e], ms[u]);
+          ro[e] = root_value((vc[u] >> (8 * e)) & 255u);
+          const float r = __fmul_rn(ro[e], vs[u]);
+          v[u][e] = __fmul_rn(r, r);
+        }
+      }
+      float size[4], r[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float gc = __fmul_rn(g[u][e], c);
+        const float a = __fmul_rn(k.b1, m[u][e]), b = __fmul_rn(k.ob1, gc);
+        size[e] = fabsf(a) + fabsf(b);
+        m[u][e] = __fadd_rn(a, b);
+        v[u][e] = __fadd_rn(__fmul_rn(k.b2, v[u][e]), __fmul_rn(__fmul_rn(gc, gc), k.ob2));
+        r[e] = __fsqrt_rn(v[u][e]);
+        const float x = __fdiv_rn(m[u][e], __fadd_rn(__fmul_rn(r[e], root), k.eps));
+        p[u][e] = __fsub_rn(__fmul_rn(p[u][e], decay), __fmul_rn(x, scale));
+      }
+      store4(E.p, i, n, vec, PDT, p[u]);
+      if (E.copy) store4(E.copy, i, n, vec, k.cdt, p[u]);
+      if constexpr (BITS == 32) {
+        store4(E.m, i, n, vec, GM_F32, m[u]);
+        store4(E.v, i, n, vec, GM_F32, v[u]);
+      } else {
+        if (left <= u * kGroup8) continue;   // the whole warp
+        // |x| as unsigned bits orders like the values; a NaN is above all of them
+        uint32_t am = 0, as = 0, ar = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          am = max(am, __float_as_uint(fabsf(m[u][e])));
+          as = max(as, __float_as_uint(size[e]));
+          ar = max(ar, __float_as_uint(fabsf(r[e])));
+        }
+        const float tm = __uint_as_float(__reduce_max_sync(0xffffffffu, am));
+        const float ts = __uint_as_float(__reduce_max_sync(0xffffffffu, as));
+        const float tr = __uint_as_float(__reduce_max_sync(0xffffffffu, ar));
+        float sm = scale_of(tm, 1.0f / kTopM), sv = scale_of(tr, 1.0f / kTopR);
+        const float im = __frcp_rn(sm), iv = __frcp_rn(sv);
+        // The stored codes are those of m and r in fp64 (each product and sum rounded
+        // singly: true ties occur, r / max r is a quotient of short numbers after the
+        // first step). fp32 decides a code unless its value lies so close to a border
+        // that its error could cross it; then the group is redone in fp64. Errors, u = 2^-24: m is off by 5 u size
+        // at most (two products of three roundings, one sum), m / sm by that and by
+        // sm's own relative error, 5 u ts / tm, plus a few u; r by 8 u.
+        const float rho = tm > 0.f ? __fdividef(ts, tm) + 1.f : 0.f;
+        // Near fp32's subnormals these bounds do not hold: 2^-90 and 2^-40 keep the
+        // smallest element that gets a code (2^-18 of the top) and its square above them.
+        bool near = (tm > 0.f && tm < 8.1e-28f) || (tr > 0.f && tr < 9.1e-13f);
+        uint32_t wm = 0, wv = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float y = __fmul_rn(m[u][e], im);
+          const float d = (size[e] + fabsf(m[u][e]) * rho) * (im * 4.76837158e-7f);   // 2^-21
+          const uint32_t q = e4m3x2(y - d, y + d);
+          near |= (q & 255u) != (q >> 8);
+          wm |= (q & 255u) << (8 * e);
+          const uint32_t bits = root_bits(__fmul_rn(r[e], iv));
+          const uint32_t low = bits & 0x7FFFFu;
+          near |= low - (0x40000u - 32u) <= 64u;
+          wv |= root_code(bits, v[u][e]) << (8 * e);
+        }
+        if (__any_sync(0xffffffffu, near) && tm <= 3.402823466e38f && tr <= 3.402823466e38f) {
+          const double dc = coef->c;
+          double dm[4], dv[4], xm = 0.0, xv = 0.0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const double gd = __dmul_rn((double)g[u][e], dc);
+            const double rd = (double)ro[e] * (double)vs[u], md = (double)mo[e] * (double)ms[u];
+            dm[e] = __dadd_rn(__dmul_rn(k.db1, md), __dmul_rn(k.dob1, gd));
+            dv[e] = __dadd_rn(__dmul_rn(k.db2, __dmul_rn(rd, rd)), __dmul_rn(k.dob2, __dmul_rn(gd, gd)));
+            xm = fmax(xm, fabs(dm[e]));
+            xv = fmax(xv, dv[e]);
+          }
+          const double dsm = fmax(warp_max(xm) / 448.0, pow2d(-126));
+          const double dsv = fmax(sqrt(warp_max(xv)) / 1.9375, pow2d(-126));
+          wm = wv = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            wm |= e4m3_from_double(dm[e] / dsm) << (8 * e);
+            wv |= root_from_double(sqrt(dv[e]) / dsv, dv[e]) << (8 * e);
+          }
+          sm = (float)dsm;
+          sv = (float)dsv;
+        }
+        store4_codes(static_cast<uint8_t*>(E.m), i, n, vec, wm);
+        store4_codes(static_cast<uint8_t*>(E.v), i, n, vec, wv);
+        if (lane == 0) {
+          const long long grp = base / kGroup8 + u;
+          E.mscale[grp] = sm;
+          E.vscale[grp] = sv;
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------ 8-bit states to fp32
+struct UnpackEntry {
+  const uint8_t* m;
+  const uint8_t* v;
+  const float* mscale;
+  const float* vscale;
+  float* m_out;
+  float* v_out;
+  long long numel;
+};
+constexpr int kMaxUnpack = 480;
+struct UnpackTable {
+  ChunkMap<kMaxUnpack> map;
+  uint8_t vec[kMaxUnpack];
+  UnpackEntry e[kMaxUnpack];
+};
+
+__global__ void __launch_bounds__(kThreads) k_adamw_unpack8(const __grid_constant__ UnpackTable t) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int ti = 0;
+  for (int chunk = blockIdx.x; chunk < t.map.total(); chunk += gridDim.x) {
+    ti = t.map.find(chunk, ti);
+    const UnpackEntry& E = t.e[ti];
+    const long long base = (long long)(chunk - t.map.first[ti]) * kChunk + warp * (kUnroll * kGroup8);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const long long i = base + u * kGroup8 + lane * 4, n = E.numel - i;
+      if (n <= 0) continue;
+      const bool vec = t.vec[ti] && n >= 4;
+      const uint32_t mc = load4_codes(E.m, i, n, vec), vc = load4_codes(E.v, i, n, vec);
+      const float ms = E.mscale[i / kGroup8], vs = E.vscale[i / kGroup8];
+      float m[4], v[4];
+      e4m3x4_to_float(mc, m);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        m[e] = __fmul_rn(m[e], ms);
+        const float r = __fmul_rn(root_value((vc >> (8 * e)) & 255u), vs);
+        v[e] = __fmul_rn(r, r);
+      }
+      store4(E.m_out, i, n, vec, GM_F32, m);
+      store4(E.v_out, i, n, vec, GM_F32, v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- gradient norm
+// Sum of squares in fp64, exact to its roundings: a bf16, fp16 or fp32 magnitude
+// becomes a double by moving its bits (no conversion instruction, whose rate would
+// bound a 16-bit gradient). Its exponent is then short by 896, which one product by
+// 2^896 mends, subnormals included; an infinity or a NaN reads as 2^128 or more, so
+// a sum of 2^256 or more, which no fp32 norm could hold either, marks them.
+struct GradEntry {
+  const void* g;
+  long long numel;
+};
+constexpr int kMaxGrads = 1024;
+constexpr int kNormChunk = 16384;           // elements
+constexpr int kNormBlocks = 4 * 148;        // CTAs, and partial sums, of a launch
+struct GradTable {
+  ChunkMap<kMaxGrads> map;
+  uint8_t kind[kMaxGrads];                  // dtype, plus 4 when 16-byte loads are aligned
+  GradEntry e[kMaxGrads];
+};
+
+__device__ __forceinline__ double widen(float x) {
+  const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+  return __hiloint2double((int)(b >> 3), (int)(b << 29)) * pow2d(896);
+}
+__device__ __forceinline__ void add_square(double& acc, float x) {
+  const double d = widen(x);
+  acc = fma(d, d, acc);
+}
+
+template <int DT>
+__device__ __forceinline__ void norm_chunk(const void* g, long long base, long long numel, bool vec,
+                                           double (&acc)[2]) {
+  constexpr int W = DT == GM_F32 ? 4 : 8;   // elements of 16 bytes
+  const long long end = min(numel, base + kNormChunk);
+  if (!vec) {
+    for (long long i = base + threadIdx.x; i < end; i += kThreads) add_square(acc[0], one<DT>(g, i));
+    return;
+  }
+  const long long full = base + (end - base) / W * W;
+#pragma unroll 4
+  for (long long i = base + (long long)threadIdx.x * W; i < full; i += kThreads * W) {
+    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(g) + i * (16 / W));
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (DT == GM_F32) {
+        add_square(acc[j & 1], __uint_as_float(x[j]));
+      } else {
+        add_square(acc[0], h16_to_float((uint16_t)(x[j] & 0xFFFFu), DT == GM_F16));
+        add_square(acc[1], h16_to_float((uint16_t)(x[j] >> 16), DT == GM_F16));
+      }
+    }
+  }
+  for (long long i = full + threadIdx.x; i < end; i += kThreads) add_square(acc[0], one<DT>(g, i));
+}
+
+__device__ __forceinline__ double block_sum(double x) {
+  __shared__ double part[kWarps];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+  __syncthreads();
+  double s = 0.0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) s += part[w];
+  return s;
+}
+
+__global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ GradTable t,
+                                                        double* __restrict__ part) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  double acc[2] = {0.0, 0.0};
+  int ti = 0;
+  for (int chunk = blockIdx.x; chunk < t.map.total(); chunk += gridDim.x) {
+    ti = t.map.find(chunk, ti);
+    const long long base = (long long)(chunk - t.map.first[ti]) * kNormChunk;
+    const bool vec = (t.kind[ti] & 4) != 0;
+    switch (t.kind[ti] & 3) {
+      case GM_F32: norm_chunk<GM_F32>(t.e[ti].g, base, t.e[ti].numel, vec, acc); break;
+      case GM_BF16: norm_chunk<GM_BF16>(t.e[ti].g, base, t.e[ti].numel, vec, acc); break;
+      default: norm_chunk<GM_F16>(t.e[ti].g, base, t.e[ti].numel, vec, acc); break;
+    }
+  }
+  const double s = block_sum(acc[0] + acc[1]);
+  if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+// The partial sums in a fixed order, so that equal gradients give equal bits.
+__global__ void __launch_bounds__(kThreads) k_grad_norm_join(int n, const double* __restrict__ part,
+                                                             double max_norm, float* norm,
+                                                             double* scale, int32_t* status) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  double acc = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) acc += part[i];
+  const double s = block_sum(acc);
+  if (threadIdx.x) return;
+  const double r = sqrt(s);
+  const bool ok = s < pow2d(256) && (float)r <= 3.402823466e38f;
+  *norm = ok ? (float)r : __int_as_float(0x7f800000);
+  *scale = ok ? fmin(1.0, max_norm / (r + 1e-6)) : 0.0;
+  *status = ok ? GM_OK : GM_E_NONFINITE;
+}
+
+template <typename M>
+cudaError_t build_map(M& map, int count, const int64_t* numel_at, size_t stride, int chunk) {
+  long long at = 0;
+  map.count = count;
+  for (int i = 0; i < count; ++i) {
+    map.first[i] = (int)at;
+    const int64_t n = *reinterpret_cast<const int64_t*>(reinterpret_cast<const uint8_t*>(numel_at) + i * stride);
+    at += cdivll(n, chunk);
+    if (at > 0x7fffffffLL) return cudaErrorInvalidValue;
+  }
+  map.first[count] = (int)at;
+  return cudaSuccess;
+}
+
+bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+int width(int dt) { return dt == GM_F32 ? 4 : 2; }
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_after(void (*kernel)(KArgs...), int grid, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+using AdamWKernel = void (*)(Table, Consts, const Coef*);
+template <int BITS>
+AdamWKernel pick(int pdt, int gdt) {
+  static const AdamWKernel k[3][3] = {
+      {k_adamw<GM_F32, GM_F32, BITS>, k_adamw<GM_F32, GM_BF16, BITS>, k_adamw<GM_F32, GM_F16, BITS>},
+      {k_adamw<GM_BF16, GM_F32, BITS>, k_adamw<GM_BF16, GM_BF16, BITS>, k_adamw<GM_BF16, GM_F16, BITS>},
+      {k_adamw<GM_F16, GM_F32, BITS>, k_adamw<GM_F16, GM_BF16, BITS>, k_adamw<GM_F16, GM_F16, BITS>}};
+  return k[pdt][gdt];
+}
+
+}  // namespace
+
+cudaError_t launch_adamw_begin(const gm_adamw_params& prm, int64_t* step, const int32_t* skip,
+                               void* scratch, cudaStream_t s) {
+  k_adamw_begin<<<1, 1, 0, s>>>(prm.lr, prm.beta1, prm.beta2, prm.wd, prm.clip, prm.lr_dev, skip, step,
+                                static_cast<Coef*>(scratch));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_adamw(int count, const gm_adamw_tensor* tensors, int pdt, int gdt, int cdt,
+                         const gm_adamw_params& prm, const void* scratch, cudaStream_t s) {
+  const Consts k{(float)prm.beta1, (float)(1.0 - prm.beta1), (float)prm.beta2,
+                 (float)(1.0 - prm.beta2), (float)prm.eps, prm.beta1, 1.0 - prm.beta1, prm.beta2,
+                 1.0 - prm.beta2, cdt};
+  const AdamWKernel kernel = prm.bits == 32 ? pick<32>(pdt, gdt) : pick<8>(pdt, gdt);
+  const int state = prm.bits == 32 ? 16 : 4;
+  for (int at = 0; at < count; at += kMaxTensors) {
+    const int n = count - at < kMaxTensors ? count - at : kMaxTensors;
+    Table t;
+    cudaError_t e = build_map(t.map, n, &tensors[at].numel, sizeof(gm_adamw_tensor), kChunk);
+    if (e != cudaSuccess) return e;
+    for (int i = 0; i < n; ++i) {
+      const gm_adamw_tensor& x = tensors[at + i];
+      t.e[i] = {x.p, x.g, x.m, x.v, x.mscale, x.vscale, x.copy, x.numel};
+      t.vec[i] = aligned_to(x.p, 4 * width(pdt)) && aligned_to(x.g, 4 * width(gdt)) &&
+                 aligned_to(x.m, state) && aligned_to(x.v, state) &&
+                 aligned_to(x.copy, 4 * width(cdt));
+    }
+    const int total = t.map.first[n];
+    const int grid = total < 8 * sm_count() ? total : 8 * sm_count();
+    e = launch_after(kernel, grid, s, t, k, static_cast<const Coef*>(scratch));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_adamw_unpack8(int count, const gm_adamw_state8* tensors, cudaStream_t s) {
+  for (int at = 0; at < count; at += kMaxUnpack) {
+    const int n = count - at < kMaxUnpack ? count - at : kMaxUnpack;
+    UnpackTable t;
+    cudaError_t e = build_map(t.map, n, &tensors[at].numel, sizeof(gm_adamw_state8), kChunk);
+    if (e != cudaSuccess) return e;
+    for (int i = 0; i < n; ++i) {
+      const gm_adamw_state8& x = tensors[at + i];
+      t.e[i] = {x.m, x.v, x.mscale, x.vscale, x.m_out, x.v_out, x.numel};
+      t.vec[i] = aligned_to(x.m, 4) && aligned_to(x.v, 4) && aligned_to(x.m_out, 16) &&
+                 aligned_to(x.v_out, 16);
+    }
+    const int total = t.map.first[n];
+    const int grid = total < 8 * sm_count() ? total : 8 * sm_count();
+    k_adamw_unpack8<<<grid, kThreads, 0, s>>>(t);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+int grad_norm_partials(int count) { return cdiv(count, kMaxGrads) * kNormBlocks; }
+
+cudaError_t launch_grad_norm(int count, const gm_grad* grads, double max_norm, float* norm,
+                             double* scale, int32_t* status, double* part, cudaStream_t s) {
+  int used = 0;
+  for (int at = 0; at < count; at += kMaxGrads) {
+    const int n = count - at < kMaxGrads ? count - at : kMaxGrads;
+    GradTable t;
+    cudaError_t e = build_map(t.map, n, &grads[at].numel, sizeof(gm_grad), kNormChunk);
+    if (e != cudaSuccess) return e;
+    for (int i = 0; i < n; ++i) {
+      const gm_grad& x = grads[at + i];
+      t.e[i] = {x.g, x.numel};
+      t.kind[i] = (uint8_t)(x.dtype | (aligned_to(x.g, 16) ? 4 : 0));
+    }
+    const int total = t.map.first[n];
+    const int grid = total < kNormBlocks ? total : kNormBlocks;
+    k_grad_norm<<<grid, kThreads, 0, s>>>(t, part + used);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    used += grid;
+  }
+  return launch_after(k_grad_norm_join, 1, s, used, (const double*)part, max_norm, norm, scale, status);
+}
+
+}  // namespace gm

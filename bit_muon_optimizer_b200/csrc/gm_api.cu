@@ -113,6 +113,11 @@ bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255) =
 // NULL counts as aligned (optional arguments are checked for presence separately).
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+constexpr int kMaxList = 65536;   // tensors of a multi-tensor call
+bool aligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+bool dtype_ok(int dt) { return dt == GM_F32 || dt == GM_BF16 || dt == GM_F16; }
+size_t dtype_bytes(int dt) { return dt == GM_F32 ? 4 : 2; }
+
 }  // namespace
 
 gm_status set_error(gm_status s, const char* fmt, ...) {
@@ -655,6 +660,114 @@ gm_status gm_weight_update(int B, int m, int n, float eta, float wd, const void*
   GM_DEVICE();
   GM_CUDA(launch_weight_update(B, m, n, eta, wd, O, (int)odt, W, skip, skip_stride,
                                reinterpret_cast<cudaStream_t>(stream)));
+  return GM_OK;
+}
+
+size_t gm_grad_norm_workspace_bytes(int count) {
+  return count >= 1 && count <= kMaxList ? al256((size_t)grad_norm_partials(count) * sizeof(double)) : 0;
+}
+
+gm_status gm_grad_norm(int count, const gm_grad* grads, double max_norm, float* norm, double* scale,
+                       int32_t* dev_status, void* ws, size_t ws_bytes, gm_stream_t stream) {
+  GM_CHECK_ARG(count >= 1 && count <= kMaxList, "count=%d out of [1, %d]", count, kMaxList);
+  GM_CHECK_ARG(grads && norm && scale && dev_status, "NULL list or output");
+  GM_CHECK_ARG(max_norm > 0.0, "max_norm must be positive (infinity: no clipping)");
+  for (int i = 0; i < count; ++i) {
+    const gm_grad& x = grads[i];
+    GM_CHECK_ARG(dtype_ok(x.dtype), "bad dtype of gradient %d", i);
+    GM_CHECK_ARG(x.g && x.numel >= 1, "NULL or empty gradient %d", i);
+    GM_CHECK_ARG(aligned(x.g, dtype_bytes(x.dtype)), "gradient %d is not aligned to its elements", i);
+  }
+  const size_t need = gm_grad_norm_workspace_bytes(count);
+  if (!ws || ws_bytes < need || !aligned256(ws))
+    return set_error(GM_E_WORKSPACE, "workspace needs %zu bytes, 256-aligned", need);
+  GM_DEVICE();
+  GM_CUDA(launch_grad_norm(count, grads, max_norm, norm, scale, dev_status, static_cast<double*>(ws),
+                           reinterpret_cast<cudaStream_t>(stream)));
+  return GM_OK;
+}
+
+static gm_status adamw_params_check(const gm_adamw_params* p) {
+  GM_CHECK_ARG(p, "NULL params");
+  GM_CHECK_ARG(p->bits == 32 || p->bits == 8, "bits=%d: states have 32 or 8 bits", p->bits);
+  GM_CHECK_ARG(std::isfinite(p->lr) && std::isfinite(p->wd), "lr and wd must be finite");
+  GM_CHECK_ARG(p->beta1 >= 0.0 && p->beta1 < 1.0 && p->beta2 >= 0.0 && p->beta2 < 1.0,
+               "beta1 and beta2 lie in [0, 1)");
+  GM_CHECK_ARG(std::isfinite(p->eps) && p->eps >= 1e-30, "eps must be finite and at least 1e-30");
+  GM_CHECK_ARG(aligned(p->clip, 8) && aligned(p->lr_dev, 4), "misaligned clip or lr_dev");
+  return GM_OK;
+}
+
+static gm_status adamw_list_check(int count, const gm_adamw_tensor* t, gm_dtype pdt, gm_dtype gdt,
+                                  gm_dtype cdt, int bits) {
+  GM_CHECK_ARG(count >= 1 && count <= kMaxList, "count=%d out of [1, %d]", count, kMaxList);
+  GM_CHECK_ARG(t, "NULL list");
+  GM_CHECK_ARG(dtype_ok(pdt) && dtype_ok(gdt) && dtype_ok(cdt), "bad dtype");
+  for (int i = 0; i < count; ++i) {
+    const gm_adamw_tensor& x = t[i];
+    GM_CHECK_ARG(x.p && x.g && x.m && x.v && x.numel >= 1, "NULL or empty array of tensor %d", i);
+    GM_CHECK_ARG(aligned(x.p, dtype_bytes(pdt)) && aligned(x.g, dtype_bytes(gdt)) &&
+                     aligned(x.copy, dtype_bytes(cdt)),
+                 "an array of tensor %d is not aligned to its elements", i);
+    if (bits == 32)
+      GM_CHECK_ARG(aligned(x.m, 4) && aligned(x.v, 4), "a state of tensor %d is not aligned", i);
+    else
+      GM_CHECK_ARG(x.mscale && x.vscale && aligned(x.mscale, 4) && aligned(x.vscale, 4),
+                   "NULL or misaligned scales of tensor %d", i);
+  }
+  return GM_OK;
+}
+
+gm_status gm_adamw_begin(const gm_adamw_params* params, int64_t* step, const int32_t* skip,
+                         void* scratch, gm_stream_t stream) {
+  const gm_status chk = adamw_params_check(params);
+  if (chk != GM_OK) return chk;
+  GM_CHECK_ARG(step && scratch, "NULL step or scratch");
+  GM_CHECK_ARG(aligned(step, 8) && aligned(skip, 4) && al16(scratch), "misaligned step, skip or scratch");
+  GM_DEVICE();
+  GM_CUDA(launch_adamw_begin(*params, step, skip, scratch, reinterpret_cast<cudaStream_t>(stream)));
+  return GM_OK;
+}
+
+gm_status gm_adamw_apply(int count, const gm_adamw_tensor* tensors, gm_dtype pdt, gm_dtype gdt,
+                         gm_dtype cdt, const gm_adamw_params* params, const void* scratch,
+                         gm_stream_t stream) {
+  gm_status chk = adamw_params_check(params);
+  if (chk != GM_OK) return chk;
+  chk = adamw_list_check(count, tensors, pdt, gdt, cdt, params->bits);
+  if (chk != GM_OK) return chk;
+  GM_CHECK_ARG(scratch && al16(scratch), "NULL or misaligned scratch");
+  GM_DEVICE();
+  GM_CUDA(launch_adamw(count, tensors, (int)pdt, (int)gdt, (int)cdt, *params, scratch,
+                       reinterpret_cast<cudaStream_t>(stream)));
+  return GM_OK;
+}
+
+gm_status gm_adamw_step(int count, const gm_adamw_tensor* tensors, gm_dtype pdt, gm_dtype gdt,
+                        gm_dtype cdt, const gm_adamw_params* params, int64_t* step,
+                        const int32_t* skip, void* scratch, gm_stream_t stream) {
+  gm_status chk = adamw_params_check(params);
+  if (chk != GM_OK) return chk;
+  chk = adamw_list_check(count, tensors, pdt, gdt, cdt, params->bits);   // before anything is enqueued
+  if (chk != GM_OK) return chk;
+  chk = gm_adamw_begin(params, step, skip, scratch, stream);
+  if (chk != GM_OK) return chk;
+  return gm_adamw_apply(count, tensors, pdt, gdt, cdt, params, scratch, stream);
+}
+
+gm_status gm_adamw_unpack8(int count, const gm_adamw_state8* tensors, gm_stream_t stream) {
+  GM_CHECK_ARG(count >= 1 && count <= kMaxList, "count=%d out of [1, %d]", count, kMaxList);
+  GM_CHECK_ARG(tensors, "NULL list");
+  for (int i = 0; i < count; ++i) {
+    const gm_adamw_state8& x = tensors[i];
+    GM_CHECK_ARG(x.m && x.v && x.mscale && x.vscale && x.m_out && x.v_out && x.numel >= 1,
+                 "NULL or empty array of tensor %d", i);
+    GM_CHECK_ARG(aligned(x.mscale, 4) && aligned(x.vscale, 4) && aligned(x.m_out, 4) &&
+                     aligned(x.v_out, 4),
+                 "a misaligned array of tensor %d", i);
+  }
+  GM_DEVICE();
+  GM_CUDA(launch_adamw_unpack8(count, tensors, reinterpret_cast<cudaStream_t>(stream)));
   return GM_OK;
 }
 

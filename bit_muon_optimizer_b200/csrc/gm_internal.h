@@ -6,6 +6,8 @@
 
 #include <cudaTypedefs.h>
 
+#include "../../include/gmuon.h"
+
 namespace gm {
 
 // The driver's cuTensorMapEncodeTiled (NULL if the driver does not provide it).
@@ -126,6 +128,17 @@ cudaError_t launch_mulaw_quant4(int B, int m, int n, float mu, const float* X, u
                                 float* gscale, cudaStream_t s);
 cudaError_t launch_mulaw_dequant4(int B, int m, int n, float mu, const uint8_t* codes4,
                                   const float* gscale, float* X, cudaStream_t s);
+
+// AdamW and the gradient norm (gm_adamw.cu). launch_adamw_begin writes the step's
+// coefficients to scratch, which the launches of launch_adamw read.
+cudaError_t launch_adamw_begin(const gm_adamw_params& prm, int64_t* step, const int32_t* skip,
+                               void* scratch, cudaStream_t s);
+cudaError_t launch_adamw(int count, const gm_adamw_tensor* tensors, int pdt, int gdt, int cdt,
+                         const gm_adamw_params& prm, const void* scratch, cudaStream_t s);
+cudaError_t launch_adamw_unpack8(int count, const gm_adamw_state8* tensors, cudaStream_t s);
+int grad_norm_partials(int count);   // fp64 partial sums
+cudaError_t launch_grad_norm(int count, const gm_grad* grads, double max_norm, float* norm,
+                             double* scale, int32_t* status, double* part, cudaStream_t s);
 
 // Standalone NS input: scale = 1/(|X|_F + eps) per matrix, then the wide
 // 16-bit copy Y = round(scale * X) (transposed when m > n).

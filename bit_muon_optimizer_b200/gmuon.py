@@ -8,10 +8,13 @@ this module fails loudly when the library has not been built.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 
+import numpy as np
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -106,6 +109,21 @@ _sig("gm_ns_flops", c_int, [c_int, c_int, c_int, c_int, vp, c_int,
                             ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_int)])
 _sig("gm_device_errors", c_int, [vp])
 _sig("gm_test_wait_timeout", c_int, [vp, vp, ctypes.c_int64, vp])
+
+
+class AdamWParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("wd", ctypes.c_double), ("bits", c_int), ("clip", vp),
+                ("lr_dev", vp)]
+
+
+ADAMW_SCRATCH_BYTES = 64
+_sig("gm_grad_norm_workspace_bytes", c_size_t, [c_int])
+_sig("gm_grad_norm", c_int, [c_int, vp, ctypes.c_double, vp, vp, vp, vp, c_size_t, vp])
+_sig("gm_adamw_step", c_int, [c_int, vp, c_int, c_int, c_int, ctypes.POINTER(AdamWParams), vp, vp, vp, vp])
+_sig("gm_adamw_begin", c_int, [ctypes.POINTER(AdamWParams), vp, vp, vp, vp])
+_sig("gm_adamw_apply", c_int, [c_int, vp, c_int, c_int, c_int, ctypes.POINTER(AdamWParams), vp, vp])
+_sig("gm_adamw_unpack8", c_int, [c_int, vp, vp])
 
 
 class GmuonError(RuntimeError):
@@ -679,3 +697,241 @@ class GraspStep:
         N, Mp = min(self.m, self.n), max(self.m, self.n)
         dt = torch.float16 if self.ns == GM_NS_GRAM else torch.bfloat16
         return self._view(self.layout.X, (self.B, N, Mp), dt)
+
+
+# ------------------------------------------------- AdamW over lists of tensors
+
+def _on(device):
+    """The library works on the current device: makes `device` that, where it is not."""
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _list_of(tensors, name, dtypes, device=None, numels=None):
+    """Checks a list of non-empty contiguous CUDA tensors on one device."""
+    if not isinstance(tensors, (list, tuple)) or not tensors:
+        raise ValueError(f"{name}: a non-empty list of tensors expected")
+    if numels is not None and len(tensors) != len(numels):
+        raise ValueError(f"{name}: expected {len(numels)} tensors, got {len(tensors)}")
+    dev = tensors[0].device if device is None else device
+    for i, t in enumerate(tensors):
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name}[{i}]: dtype {t.dtype} is not one of {tuple(dtypes)}")
+        n = t.numel()
+        if n == 0 if numels is None else n != numels[i]:
+            raise ValueError(f"{name}[{i}]: {n} elements"
+                             + ("" if numels is None else f", expected {numels[i]}"))
+        if not t.is_cuda:
+            raise ValueError(f"{name}[{i}]: expected a CUDA tensor")
+        if t.device != dev:
+            raise ValueError(f"{name}[{i}]: on {t.device}, the others are on {dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}]: expected a contiguous tensor")
+    return dev
+
+
+def _scalar(t, dtype, name, device):
+    """Checks a one-element tensor whose address goes to the library."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() != 1:
+        raise ValueError(f"{name}: expected a one-element {dtype} tensor")
+    if t.device != device:
+        raise ValueError(f"{name}: expected on {device}, got {t.device}")
+
+
+@dataclass
+class GradNorm:
+    """The result of ``grad_norm``, on the device: ``norm`` f32 [1], ``scale`` f64
+    [1] (the clip factor), ``status`` int32 [1] (GM_E_NONFINITE when a gradient
+    holds a NaN or infinity), and the call's workspace. ``AdamWStep`` takes the
+    whole, ``weight_update`` the status as its skip flag."""
+    norm: torch.Tensor
+    scale: torch.Tensor
+    status: torch.Tensor
+    ws: torch.Tensor
+
+
+def grad_norm(grads, max_norm=None, out=None) -> GradNorm:
+    """Norm over all elements of a list of gradients (fp32, bf16, fp16, mixed), and
+    min(1, max_norm / (norm + 1e-6)) (1 without ``max_norm``). ``out``: an earlier
+    result of a list of at most this length, to write into."""
+    dev = _list_of(grads, "grads", _DT)
+    n = len(grads)
+    table = np.empty((n, 3), dtype=np.int64)
+    table[:, 0] = [t.data_ptr() for t in grads]
+    table[:, 1] = [t.numel() for t in grads]
+    table[:, 2] = [_DT[t.dtype] for t in grads]
+    nb = int(lib.gm_grad_norm_workspace_bytes(n))
+    if out is None:
+        buf = torch.empty(256 + nb, dtype=torch.uint8, device=dev)
+        out = GradNorm(buf[8:12].view(torch.float32), buf[0:8].view(torch.float64),
+                       buf[12:16].view(torch.int32), buf[256:])
+    else:
+        _scalar(out.norm, torch.float32, "out.norm", dev)
+        _scalar(out.scale, torch.float64, "out.scale", dev)
+        _scalar(out.status, torch.int32, "out.status", dev)
+        _ws_fits(out.ws, nb, "out.ws")
+        if out.ws.device != dev:
+            raise ValueError(f"out.ws: expected on {dev}, got {out.ws.device}")
+    with _on(dev):
+        _check(lib.gm_grad_norm(n, table.ctypes.data, math.inf if max_norm is None else float(max_norm),
+                                _ptr(out.norm), _ptr(out.scale), _ptr(out.status), _ptr(out.ws), nb,
+                                _stream()), "gm_grad_norm")
+    return out
+
+
+@dataclass
+class AdamWState:
+    """AdamW's moments of a list of parameters, on the device. ``bits`` 32: ``m``,
+    ``v`` fp32; 8: uint8 codes with fp32 ``mscale``, ``vscale`` per 128 elements
+    (the formats of gm_adamw_step). ``step``: completed steps, int64 [1]."""
+    bits: int
+    m: list
+    v: list
+    mscale: list
+    vscale: list
+    step: torch.Tensor
+    scratch: torch.Tensor = field(default=None, repr=False)
+
+    def __post_init__(self):
+        if self.bits not in (32, 8):
+            raise ValueError(f"bits: 32 or 8 expected, got {self.bits}")
+        if self.scratch is None:
+            self.scratch = torch.zeros(ADAMW_SCRATCH_BYTES, dtype=torch.uint8, device=self.step.device)
+
+    @staticmethod
+    def zeros(params, bits=32) -> "AdamWState":
+        """The state before the first step of ``params`` (a list of tensors)."""
+        if not params:
+            raise ValueError("params: a non-empty list of tensors expected")
+        dev = params[0].device
+        numels = [p.numel() for p in params]
+
+        def arena(dtype, per=1):   # one allocation, each tensor on a 256-element boundary
+            at, spans = 0, []
+            for n in numels:
+                spans.append((at, -(-n // per)))
+                at += -(-spans[-1][1] // 256) * 256
+            flat = torch.zeros(at, dtype=dtype, device=dev)
+            return [flat[a:a + n] for a, n in spans]
+        if bits == 32:
+            kept = [arena(torch.float32), arena(torch.float32), [], []]
+        else:
+            kept = [arena(torch.uint8), arena(torch.uint8), arena(torch.float32, GROUP),
+                    arena(torch.float32, GROUP)]
+        return AdamWState(bits, *kept, torch.zeros(1, dtype=torch.int64, device=dev))
+
+    def tensors(self):
+        return [*self.m, *self.v, *self.mscale, *self.vscale, self.step]
+
+    def clone(self):
+        c = lambda ts: [t.clone() for t in ts]                           # noqa: E731
+        return AdamWState(self.bits, c(self.m), c(self.v), c(self.mscale), c(self.vscale),
+                          self.step.clone())
+
+    def check(self, numels, dev):
+        """Raises ValueError unless the state fits tensors of `numels` elements."""
+        kept = (torch.float32,) if self.bits == 32 else (torch.uint8,)
+        _list_of(self.m, "m", kept, dev, numels)
+        _list_of(self.v, "v", kept, dev, numels)
+        if self.bits == 8:
+            groups = [-(-n // GROUP) for n in numels]
+            _list_of(self.mscale, "mscale", (torch.float32,), dev, groups)
+            _list_of(self.vscale, "vscale", (torch.float32,), dev, groups)
+        _scalar(self.step, torch.int64, "step", dev)
+        if self.scratch.device != dev or not self.scratch.is_contiguous():
+            raise ValueError(f"scratch: a contiguous tensor on {dev} expected")
+        _ws_fits(self.scratch, ADAMW_SCRATCH_BYTES, "scratch")
+
+    def moments(self, out=None):
+        """(m, v) in fp32, two lists: the state's own tensors with 32-bit states, what
+        the codes stand for with 8-bit ones (gm_adamw_unpack8; ``out``: two lists of
+        fp32 tensors to write)."""
+        if self.bits == 32:
+            if out is not None:
+                raise ValueError("out: 32-bit moments are the state's own tensors")
+            return self.m, self.v
+        numels = [t.numel() for t in self.m]
+        dev = self.step.device
+        self.check(numels, dev)
+        if out is None:
+            out = tuple([torch.empty(n, dtype=torch.float32, device=dev) for n in numels]
+                        for _ in range(2))
+        mo, vo = out
+        _list_of(mo, "out[0]", (torch.float32,), dev, numels)
+        _list_of(vo, "out[1]", (torch.float32,), dev, numels)
+        table = np.empty((len(numels), 7), dtype=np.int64)
+        for j, ts in enumerate((self.m, self.v, self.mscale, self.vscale, mo, vo)):
+            table[:, j] = [t.data_ptr() for t in ts]
+        table[:, 6] = numels
+        with _on(dev):
+            _check(lib.gm_adamw_unpack8(len(numels), table.ctypes.data, _stream()), "gm_adamw_unpack8")
+        return mo, vo
+
+
+class AdamWStep:
+    """Marshals gm_adamw_step: ``step(state, params, grads)`` updates ``params`` and
+    ``state`` in place, every tensor of the lists in one launch (one per combination
+    of dtypes). params and grads: fp32, bf16 or fp16, each gradient of its
+    parameter's size."""
+
+    def __init__(self, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, wd=0.01):
+        self.lr, self.betas, self.eps, self.wd = float(lr), (float(betas[0]), float(betas[1])), \
+            float(eps), float(wd)
+
+    def __call__(self, state: AdamWState, params, grads, copies=None, clip: GradNorm | None = None,
+                 skip=None, lr=None):
+        """``copies``: 16-bit (or fp32) tensors that receive the new parameters rounded;
+        ``clip``: a ``grad_norm`` result, whose factor scales the gradients and whose
+        status makes the call change nothing; ``skip``: such a flag (int32 [1]) alone;
+        ``lr``: this step's rate instead of the object's, a number or an fp32 [1]
+        tensor on the device (read when the step runs, for captured graphs)."""
+        dev = _list_of(params, "params", _DT)
+        numels = [p.numel() for p in params]
+        _list_of(grads, "grads", _DT, dev, numels)
+        state.check(numels, dev)
+        if copies is not None:
+            _list_of(copies, "copies", _DT, dev, numels)
+        if clip is not None:
+            if skip is not None:
+                raise ValueError("skip: clip brings its own flag")
+            skip = clip.status
+            _scalar(clip.scale, torch.float64, "clip.scale", dev)
+        if skip is not None:
+            _scalar(skip, torch.int32, "skip", dev)
+        lr_dev = None
+        if isinstance(lr, torch.Tensor):
+            _scalar(lr, torch.float32, "lr", dev)
+            lr_dev, lr = lr.data_ptr(), None
+        n = len(numels)
+        table = np.zeros((n, 8), dtype=np.int64)
+        columns = [params, grads, state.m, state.v]
+        if state.bits == 8:
+            columns += [state.mscale, state.vscale]
+        for j, ts in enumerate(columns):
+            table[:, j] = [t.data_ptr() for t in ts]
+        if copies is not None:
+            table[:, 6] = [t.data_ptr() for t in copies]
+        table[:, 7] = numels
+        if len(set(table[:, 0].tolist())) != n or len(set(table[:, 2].tolist())) != n:
+            raise ValueError("params: a tensor is in the list more than once")
+        prm = AdamWParams(self.lr if lr is None else float(lr), *self.betas, self.eps, self.wd,
+                          state.bits, clip.scale.data_ptr() if clip is not None else None, lr_dev)
+        kinds = {}
+        for i in range(n):
+            key = (_DT[params[i].dtype], _DT[grads[i].dtype],
+                   _DT[copies[i].dtype] if copies is not None else GM_F32)
+            kinds.setdefault(key, []).append(i)
+        with _on(dev):
+            s = _stream()
+            if len(kinds) == 1:
+                (key, _), = kinds.items()
+                _check(lib.gm_adamw_step(n, table.ctypes.data, *key, ctypes.byref(prm), _ptr(state.step),
+                                         _ptr(skip), _ptr(state.scratch), s), "gm_adamw_step")
+                return
+            _check(lib.gm_adamw_begin(ctypes.byref(prm), _ptr(state.step), _ptr(skip),
+                                      _ptr(state.scratch), s), "gm_adamw_begin")
+            for key, at in kinds.items():
+                part = np.ascontiguousarray(table[at])
+                _check(lib.gm_adamw_apply(len(at), part.ctypes.data, *key, ctypes.byref(prm),
+                                          _ptr(state.scratch), s), "gm_adamw_apply")

@@ -389,6 +389,104 @@ gm_status gm_grasp_orth_peers(int B, int m, int n, const gm_grasp_params* params
                               gm_dtype odt, void* ws, size_t ws_bytes, gm_stream_t stream);
 
 /*
+ * Global norm of a list of gradients, and the factor that clips them:
+ *   norm = sqrt(sum over all elements of g^2)   (sums in fp64, in a fixed order)
+ *   scale = min(1, max_norm / (norm + 1e-6))    (INFINITY as max_norm: 1)
+ *   grads: host array of `count` entries (1 <= count <= 65536), each a device
+ *   array of numel >= 1 elements of dtype (element alignment suffices).
+ *   norm f32 [1], scale f64 [1], dev_status int32 [1] (device): GM_OK, or
+ *   GM_E_NONFINITE when a gradient holds a NaN or infinity or the norm passes
+ *   fp32's range (norm = infinity, scale = 0). gm_adamw_step and
+ *   gm_weight_update take dev_status as their skip flag.
+ *   ws >= gm_grad_norm_workspace_bytes(count), 256-byte aligned; every byte that
+ *   is read is written first. The host array may be reused once the call returns.
+ */
+typedef struct {
+  const void* g;
+  int64_t numel;
+  gm_dtype dtype;
+} gm_grad;
+size_t gm_grad_norm_workspace_bytes(int count);
+gm_status gm_grad_norm(int count, const gm_grad* grads, double max_norm, float* norm, double* scale,
+                       int32_t* dev_status, void* ws, size_t ws_bytes, gm_stream_t stream);
+
+/*
+ * One AdamW step of many tensors at once, for the parameters that a Muon step
+ * does not take (embeddings, heads, norms, biases) or a whole set. With t =
+ * *step + 1 and c = *clip (1 when NULL), per element:
+ *   g <- c g;  m <- beta1 m + (1 - beta1) g;  v <- beta2 v + (1 - beta2) g^2
+ *   p <- (1 - lr wd) p - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32, p rounded once to its dtype.
+ *   tensors: host array of `count` entries (1 <= count <= 65536; may be reused once
+ *   the call returns) of device arrays of numel >= 1 elements, element alignment
+ *   sufficing (arrays that are not 16-byte aligned move element by element):
+ *     p [numel] of pdt, in place; g [numel] of gdt; copy (nullable): the new p
+ *     rounded to cdt (a 16-bit working copy);
+ *     params->bits = 32: m, v f32 [numel];
+ *     params->bits = 8: m, v uint8 [numel], mscale, vscale f32 [ceil(numel / 128)],
+ *     a scale per 128 consecutive elements:
+ *       m = e4m3(code) sm, sm = max(max|m| / 448, 2^-126);
+ *       v = (f(code) sv)^2, sv = max(max sqrt(v) / 1.9375, 2^-126), f a float of 4
+ *       exponent and 4 mantissa bits without a sign: code = 16 e + i stands for
+ *       (16 + i) 2^(e - 19) when e > 0, i 2^-18 when e = 0; a v that is not zero in
+ *       fp32 gets code 1 at least.
+ *     The step uses the new m and v before they are rounded to 8 bits, and the codes
+ *     are the nearest ones (ties to even) to m / sm and sqrt(v) / sv in fp64, each
+ *     operation above rounded singly. A group that a NaN or infinity enters (or a
+ *     g^2 past fp32's range) becomes NaN as a whole.
+ *     No two entries may overlap. All-zero codes and scales are the zero state.
+ *   step int64 [1] (device): completed steps, incremented by this one; scratch:
+ *   GM_ADAMW_SCRATCH_BYTES of device memory, 16-byte aligned, that belong to this
+ *   step count (calls that overlap on the GPU need their own).
+ *   skip (device int32, nullable): when *skip is non-zero nothing is changed, the
+ *   step count included.
+ */
+#define GM_ADAMW_SCRATCH_BYTES 64
+typedef struct {
+  double lr, beta1, beta2, eps, wd;
+  int bits;                  /* states: 32 or 8 */
+  const double* clip;        /* device [1], nullable: factor of the gradients */
+  const float* lr_dev;       /* device [1], nullable: takes lr's place (a schedule under
+                                a captured graph) */
+} gm_adamw_params;
+typedef struct {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* mscale;             /* 8-bit states only */
+  float* vscale;
+  void* copy;                /* nullable */
+  int64_t numel;
+} gm_adamw_tensor;
+gm_status gm_adamw_step(int count, const gm_adamw_tensor* tensors, gm_dtype pdt, gm_dtype gdt,
+                        gm_dtype cdt, const gm_adamw_params* params, int64_t* step,
+                        const int32_t* skip, void* scratch, gm_stream_t stream);
+/*
+ * The same for lists of mixed dtypes, one call per combination: gm_adamw_begin
+ * once (step count, coefficients into scratch, the skip flag), then
+ * gm_adamw_apply for each list with the same params and scratch.
+ * gm_adamw_step = gm_adamw_begin, then one gm_adamw_apply.
+ */
+gm_status gm_adamw_begin(const gm_adamw_params* params, int64_t* step, const int32_t* skip,
+                         void* scratch, gm_stream_t stream);
+gm_status gm_adamw_apply(int count, const gm_adamw_tensor* tensors, gm_dtype pdt, gm_dtype gdt,
+                         gm_dtype cdt, const gm_adamw_params* params, const void* scratch,
+                         gm_stream_t stream);
+
+/* fp32 m and v of 8-bit AdamW states (layouts and rules as in gm_adamw_step). */
+typedef struct {
+  const uint8_t* m;
+  const uint8_t* v;
+  const float* mscale;
+  const float* vscale;
+  float* m_out;
+  float* v_out;
+  int64_t numel;
+} gm_adamw_state8;
+gm_status gm_adamw_unpack8(int count, const gm_adamw_state8* tensors, gm_stream_t stream);
+
+/*
  * Device buffers shared between the processes of one node (CUDA IPC), for the
  * receive buffers of gm_grasp_orth_peers.
  *  - gm_ipc_export: the handle of the allocation that holds dev_ptr and the
