@@ -9,6 +9,7 @@
 
 #include "gm_common.cuh"
 #include "gm_internal.h"
+#include "gm_mx4.cuh"
 
 namespace gm {
 
@@ -117,6 +118,11 @@ constexpr int kMaxList = 65536;   // tensors of a multi-tensor call
 bool aligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 bool dtype_ok(int dt) { return dt == GM_F32 || dt == GM_BF16 || dt == GM_F16; }
 size_t dtype_bytes(int dt) { return dt == GM_F32 ? 4 : 2; }
+bool mx4_shape_ok(int B, int rows, int cols) {
+  return B >= 1 && B <= 65535 && rows >= 1 && rows <= (1 << 24) && cols >= 1 && cols <= (1 << 24) &&
+         (long long)rows * cols <= (1LL << 40);
+}
+bool mx4_format_ok(int fmt) { return fmt == GM_MX4 || fmt == GM_NV4; }
 
 }  // namespace
 
@@ -660,6 +666,78 @@ gm_status gm_weight_update(int B, int m, int n, float eta, float wd, const void*
   GM_DEVICE();
   GM_CUDA(launch_weight_update(B, m, n, eta, wd, O, (int)odt, W, skip, skip_stride,
                                reinterpret_cast<cudaStream_t>(stream)));
+  return GM_OK;
+}
+
+size_t gm_mx4_codes_bytes(int B, int rows, int cols) {
+  return mx4_shape_ok(B, rows, cols) ? (size_t)B * rows * (mx4_padded(cols) / 2) : 0;
+}
+
+size_t gm_mx4_scales_bytes(int B, int rows, int cols, gm_mx4_format fmt) {
+  if (!mx4_shape_ok(B, rows, cols) || !mx4_format_ok(fmt)) return 0;
+  return (size_t)B * cdivll(rows, 128) * mx4_atoms(cols, fmt) * 512;
+}
+
+gm_status gm_mx4_quant(int B, int m, int n, const void* X, gm_dtype xdt, int64_t row_stride,
+                       int64_t batch_stride, gm_mx4_format fmt, float* gscale, uint8_t* codes,
+                       uint8_t* scales, uint8_t* codesT, uint8_t* scalesT, gm_stream_t stream) {
+  GM_CHECK_ARG(mx4_shape_ok(B, m, n), "bad shape B=%d m=%d n=%d", B, m, n);
+  GM_CHECK_ARG(mx4_format_ok(fmt) && dtype_ok(xdt), "bad format or dtype");
+  GM_CHECK_ARG(X && aligned(X, dtype_bytes(xdt)), "NULL or misaligned X");
+  GM_CHECK_ARG(row_stride >= (m > 1 ? n : 0) && batch_stride >= 0 && row_stride <= (1LL << 40) &&
+                   batch_stride <= (1LL << 42),
+               "bad strides");
+  GM_CHECK_ARG((codes != nullptr) == (scales != nullptr) && (codesT != nullptr) == (scalesT != nullptr) &&
+                   (codes || codesT),
+               "codes and scales come in pairs, one pair at least");
+  GM_CHECK_ARG(al16(codes) && al16(scales) && al16(codesT) && al16(scalesT),
+               "device arrays must be 16-byte aligned");
+  GM_CHECK_ARG(fmt == GM_MX4 || (gscale && aligned(gscale, 4)), "GM_NV4 needs gscale");
+  GM_DEVICE();
+  GM_CUDA(launch_mx4_quant(B, m, n, X, (int)xdt, row_stride, batch_stride, (int)fmt, gscale, codes,
+                           scales, codesT, scalesT, reinterpret_cast<cudaStream_t>(stream)));
+  return GM_OK;
+}
+
+gm_status gm_mx4_dequant(int B, int rows, int cols, gm_mx4_format fmt, const uint8_t* codes,
+                         const uint8_t* scales, const float* gscale, void* X_out, gm_dtype odt,
+                         gm_stream_t stream) {
+  GM_CHECK_ARG(mx4_shape_ok(B, rows, cols), "bad shape B=%d rows=%d cols=%d", B, rows, cols);
+  GM_CHECK_ARG(mx4_format_ok(fmt) && dtype_ok(odt), "bad format or dtype");
+  GM_CHECK_ARG(codes && scales && X_out, "NULL pointer");
+  GM_CHECK_ARG(al16(codes) && al16(scales) && al16(X_out), "device arrays must be 16-byte aligned");
+  GM_CHECK_ARG(fmt == GM_MX4 || (gscale && aligned(gscale, 4)), "GM_NV4 needs gscale");
+  GM_DEVICE();
+  GM_CUDA(launch_mx4_dequant(B, rows, cols, (int)fmt, codes, scales, gscale, X_out, (int)odt,
+                             reinterpret_cast<cudaStream_t>(stream)));
+  return GM_OK;
+}
+
+size_t gm_mx4_matmul_workspace_bytes(int B, int M, int N, int K) {
+  if (!mx4_shape_ok(B, M, K) || !mx4_shape_ok(B, N, K) || !mx4_shape_ok(B, M, N)) return 0;
+  return mx4_matmul_ws_bytes(B, M, N, K);
+}
+
+gm_status gm_mx4_matmul(int B, int M, int N, int K, gm_mx4_format fmt, const uint8_t* A_codes,
+                        const uint8_t* A_scales, const float* A_gscale, const uint8_t* B_codes,
+                        const uint8_t* B_scales, const float* B_gscale, void* D, gm_dtype ddt,
+                        int accumulate, void* ws, size_t ws_bytes, gm_stream_t stream) {
+  GM_CHECK_ARG(mx4_shape_ok(B, M, K) && mx4_shape_ok(B, N, K) && mx4_shape_ok(B, M, N),
+               "bad shape B=%d M=%d N=%d K=%d", B, M, N, K);
+  GM_CHECK_ARG(mx4_format_ok(fmt) && dtype_ok(ddt), "bad format or dtype");
+  GM_CHECK_ARG(accumulate == 0 || accumulate == 1, "accumulate must be 0 or 1");
+  GM_CHECK_ARG(A_codes && A_scales && B_codes && B_scales && D, "NULL pointer");
+  GM_CHECK_ARG(al16(A_codes) && al16(A_scales) && al16(B_codes) && al16(B_scales) && al16(D),
+               "device arrays must be 16-byte aligned");
+  GM_CHECK_ARG(fmt == GM_MX4 || (A_gscale && B_gscale && aligned(A_gscale, 4) && aligned(B_gscale, 4)),
+               "GM_NV4 needs both gscale");
+  const size_t need = mx4_matmul_ws_bytes(B, M, N, K);
+  if (need && (!ws || ws_bytes < need || !aligned256(ws)))
+    return set_error(GM_E_WORKSPACE, "workspace needs %zu bytes, 256-aligned", need);
+  GM_DEVICE();
+  GM_CUDA(launch_mx4_matmul(B, M, N, K, (int)fmt, A_codes, A_scales, A_gscale, B_codes, B_scales,
+                            B_gscale, D, (int)ddt, accumulate, ws,
+                            reinterpret_cast<cudaStream_t>(stream)));
   return GM_OK;
 }
 

@@ -1,0 +1,460 @@
+// Quantisation to microscaled 4-bit values and back: along the rows of a matrix,
+// along its columns (the transpose's rows), or both in one pass over it.
+//
+// GM_MX4 (blocks of 32): b = max(floor(log2 max|x|) + 127 - 2, 0), scale 2^(b-127),
+//   codes e2m1(x 2^(127-b)): every step is exact but the rounding to e2m1.
+// GM_NV4 (blocks of 16): gs = fp32(max|X| / 2688), sb = e4m3(max|x| / (6 gs)), codes
+//   e2m1(x / (sb gs)). 2688 = 6 * 448, so the largest block scale is e4m3's largest.
+//   Codes and scales are those of the exact quotients: fp32 decides unless the value
+//   lies so close to a border that fp32's error could cross it (about one in 10^5),
+//   then fp64 does (a border times sb gs has at most 31 bits: exact there).
+//
+// Both are bound by HBM: x once (2 or 4 B), 0.53 or 0.56 B per orientation; GM_NV4
+// reads x before that for the matrix scale.
+
+#include <math.h>
+
+#include "gm_common.cuh"
+#include "gm_internal.h"
+#include "gm_mx4.cuh"
+
+namespace gm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 128;
+
+// Eight consecutive elements from column c of a row of n (zeros behind its end).
+template <int DT>
+__device__ __forceinline__ void load8(const void* row, long long c, long long n, bool vec, float (&o)[8]) {
+  if (vec && c + 8 <= n) {
+    if constexpr (DT == GM_F32) {
+      const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + c);
+      const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + c + 4);
+      o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+      o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+    } else {
+      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        o[2 * j] = h16_to_float((uint16_t)(w[j] & 0xFFFFu), DT == GM_F16);
+        o[2 * j + 1] = h16_to_float((uint16_t)(w[j] >> 16), DT == GM_F16);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = c + e < n ? load_as_float(row, c + e, DT) : 0.f;
+  }
+}
+
+// --------------------------------------------------------------------- encoding
+// Codes of eight values, element 0 in the lowest nibble.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&y)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return w;
+}
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+constexpr float kBelow = 1.0f - 9.5367431640625e-7f, kAbove = 1.0f + 9.5367431640625e-7f;   // 1 -+ 2^-20
+
+// Matrix-wide constants of GM_NV4; for GM_MX4 unused.
+struct MatrixScale {
+  float gs;
+  float inv6;      // 1 / (6 gs)
+  bool exact;      // fp32 quotients would leave its normal range: decide in fp64
+};
+template <int FMT>
+__device__ __forceinline__ MatrixScale matrix_scale(const float* gscale, int b) {
+  MatrixScale g{1.f, 0.f, false};
+  if constexpr (FMT == GM_NV4) {
+    g.gs = gscale[b];
+    g.exact = !(g.gs >= 1e-28f && g.gs <= 1e28f);
+    g.inv6 = __fdiv_rn(1.0f, 6.0f * g.gs);
+  }
+  return g;
+}
+
+// The scale byte of a block whose largest magnitude is `top` (a NaN's bits lie
+// above every number's), and what its elements are multiplied by.
+template <int FMT>
+__device__ __forceinline__ uint32_t block_scale(float top, const MatrixScale& g, float& mul) {
+  if constexpr (FMT == GM_MX4) {
+    const uint32_t e = __float_as_uint(top) >> 23;   // top >= 0
+    if (e == 255u) {
+      mul = 0.f;
+      return 255u;
+    }
+    const uint32_t b = e > 2u ? e - 2u : 0u;
+    mul = __uint_as_float((254u - b) << 23);
+    return b;
+  } else {
+    mul = 0.f;
+    if (!(g.gs > 0.f && g.gs <= 3.402823466e38f)) return 0u;   // a zero matrix, or one that is NaN
+    uint32_t b;
+    bool sure = !g.exact;
+    if (sure) {
+      const float t = top * g.inv6;
+      const uint32_t q = e4m3x2(t * kBelow, t * kAbove);
+      b = q & 255u;
+      sure = b == (q >> 8);
+    }
+    if (!sure) {
+      // rn to 3 fraction bits, exponents from -6, at most 448
+      const double t = (double)top / (6.0 * (double)g.gs);
+      const int e = max((__double2hiint(t) >> 20) - 1023, -6);
+      const int k = (int)rint(fmin(t, 449.0) * __hiloint2double((3 - e + 1023) << 20, 0));
+      b = min((uint32_t)(((e + 6) << 3) + k), 126u);
+    }
+    if (b) mul = __fdiv_rn(1.0f, e4m3_value(b) * g.gs);
+    return b;
+  }
+}
+
+__device__ __forceinline__ uint32_t e2m1_exact(float x, double s) {
+  const double a = fabs((double)x) / s;
+  const uint32_t c = (a > 0.25) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0);
+  return c | (x < 0.f ? 8u : 0u);
+}
+
+// Codes of eight elements of one block.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes8(const float (&x)[8], uint32_t b, float mul, const MatrixScale& g) {
+  float y[8];
+  if constexpr (FMT == GM_MX4) {
+    if (b == 255u) return 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = x[e] * mul;
+    return e2m1x8(y);
+  } else {
+    if (b == 0u) return 0u;
+    float z[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[e] = x[e] * (mul * kBelow);
+      z[e] = x[e] * (mul * kAbove);
+    }
+    uint32_t w = e2m1x8(y);
+    if (w != e2m1x8(z) || g.exact) {
+      const double s = (double)e4m3_value(b) * (double)g.gs;
+      w = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w |= e2m1_exact(x[e], s) << (4 * e);
+    }
+    return w;
+  }
+}
+
+__device__ __forceinline__ uint32_t top8(const float (&x)[8]) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(fabsf(x[e])));
+  return a;
+}
+
+struct QuantParams {
+  int m, n;
+  const void* X;
+  long long ldx, xbs;      // elements
+  int vec;                 // rows start on 16 bytes
+  float* gscale;           // [B], GM_NV4
+  uint8_t *codes, *scales;       // along rows
+  uint8_t *codesT, *scalesT;     // along columns
+  long long tiles_m, tiles_n;
+};
+
+__device__ __forceinline__ const uint8_t* row_ptr(const QuantParams& p, int b, long long r, int es) {
+  return static_cast<const uint8_t*>(p.X) + (b * p.xbs + r * p.ldx) * es;
+}
+template <int DT>
+constexpr int kElem = DT == GM_F32 ? 4 : 2;
+
+// ------------------------------------------------------------- the matrix scale
+// gscale[b] = max over elements of fp32(|x| / 2688) by atomicMax on its bits (the
+// order does not matter; division is monotone, so this is the quotient of the
+// maximum); an infinity or a NaN leaves a NaN.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) k_mx4_top(const QuantParams p) {
+  const int b = blockIdx.y;
+  const long long c8 = (p.n + 7) / 8, items = c8 * p.m;
+  uint32_t top = 0;
+  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < items;
+       i += (long long)gridDim.x * kThreads) {
+    const long long r = i / c8, c = (i - r * c8) * 8;
+    float x[8];
+    load8<DT>(row_ptr(p, b, r, kElem<DT>), c, p.n, p.vec != 0, x);
+    top = max(top, top8(x));
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  __shared__ uint32_t part[kThreads / 32];
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kThreads / 32; ++w) top = max(top, part[w]);
+    const float t = __uint_as_float(top);
+    const float gs = t <= 3.402823466e38f ? __fdiv_rn(t, 2688.0f) : __int_as_float(0x7fffffff);
+    atomicMax(reinterpret_cast<unsigned*>(p.gscale + b), __float_as_uint(gs));
+  }
+}
+
+// -------------------------------------------------------------------- rows only
+// A warp takes 256 elements of a row per trip: lane l the eight from 8 l; the
+// block's maximum is shared by 4 (GM_MX4) or 2 lanes, a word of four scale bytes
+// gathered from 16 or 8. A CTA takes 8 rows and kRowSpan columns. Rows of the last
+// 128-row tile behind m get zero scales.
+constexpr int kRowSpan = 1024;
+template <int DT, int FMT>
+__global__ void __launch_bounds__(kThreads) k_mx4_rows(const QuantParams p, long long spans) {
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const long long r = blockIdx.x / spans * 8 + (threadIdx.x >> 5);
+  const long long c0 = blockIdx.x % spans * kRowSpan;
+  const long long np = mx4_padded(p.n), atoms = mx4_atoms(p.n, FMT);
+  constexpr int L = mx4_block(FMT) / 8;     // lanes of a block
+  uint8_t* sc = p.scales + ((b * p.tiles_m + r / 128) * atoms) * 512 + mx4_atom_byte((int)(r % 128), 0);
+  const bool live = r < p.m;
+  const MatrixScale g = matrix_scale<FMT>(p.gscale, b);
+  const void* row = row_ptr(p, b, live ? r : 0, kElem<DT>);
+  const long long n = live ? p.n : 0;
+  float x[kRowSpan / 256][8];
+#pragma unroll
+  for (int u = 0; u < kRowSpan / 256; ++u)
+    load8<DT>(row, c0 + u * 256 + lane * 8, n, p.vec != 0, x[u]);
+#pragma unroll
+  for (int u = 0; u < kRowSpan / 256; ++u) {
+    const long long c = c0 + u * 256 + lane * 8;
+    uint32_t top = top8(x[u]);
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float mul;
+    const uint32_t s = block_scale<FMT>(__uint_as_float(top), g, mul);
+    if (live && c < np)
+      *reinterpret_cast<uint32_t*>(p.codes + ((b * (long long)p.m + r) * np + c) / 2) =
+          codes8<FMT>(x[u], s, mul, g);
+    // lane 4 L i gathers the bytes of lanes 4 L i, + L, + 2 L, + 3 L
+    uint32_t w = s;
+    w |= __shfl_down_sync(0xffffffffu, s, L) << 8;
+    w |= __shfl_down_sync(0xffffffffu, s, 2 * L) << 16;
+    w |= __shfl_down_sync(0xffffffffu, s, 3 * L) << 24;
+    if (lane % (4 * L) == 0 && c < np)
+      *reinterpret_cast<uint32_t*>(sc + c / (4 * mx4_block(FMT)) * 512) = live ? w : 0u;
+  }
+}
+
+// ----------------------------------------------------------------- both or columns
+// A CTA takes a 128 x 128 tile. Each thread loads eight elements of a row at a time,
+// quantises them along the row, and leaves them in shared memory (16-bit inputs as
+// they are); then it takes two neighbouring columns of 32 rows. Scale bytes of both
+// orientations are gathered in shared memory and leave as whole atoms.
+template <int DT>
+struct TileType { using T = uint16_t; };
+template <>
+struct TileType<GM_F32> { using T = float; };
+
+template <int DT, int FMT>
+__global__ void __launch_bounds__(kThreads) k_mx4_tile(const QuantParams p) {
+  using T = typename TileType<DT>::T;
+  constexpr int BL = mx4_block(FMT), L = BL / 8, NA = kTile / (4 * BL);   // atoms of a tile: 1 or 2
+  extern __shared__ __align__(16) uint8_t dyn[];
+  T* tile = reinterpret_cast<T*>(dyn);
+  __shared__ __align__(16) uint8_t sR[NA * 512], sC[NA * 512];
+  const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long tm = blockIdx.x / p.tiles_n, tn = blockIdx.x % p.tiles_n;
+  const long long r0 = tm * kTile, c0 = tn * kTile;
+  const long long np = p.tiles_n * kTile, mp = p.tiles_m * kTile;
+  const MatrixScale g = matrix_scale<FMT>(p.gscale, b);
+  const bool rows = p.codes != nullptr;
+
+  // 16 lanes a row, 16 rows a trip
+  const int cl = (lane & 15) * 8;
+#pragma unroll 4
+  for (int it = 0; it < kTile / 16; ++it) {
+    const int rl = it * 16 + warp * 2 + (lane >> 4);
+    const long long r = r0 + rl;
+    float x[8];
+    load8<DT>(row_ptr(p, b, r < p.m ? r : 0, kElem<DT>), c0 + cl, r < p.m ? p.n : 0, p.vec != 0, x);
+    if constexpr (DT == GM_F32) {
+      *reinterpret_cast<float4*>(tile + rl * kTile + cl) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4*>(tile + rl * kTile + cl + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = (uint32_t)float_to_h16(x[2 * j], DT == GM_F16) |
+               ((uint32_t)float_to_h16(x[2 * j + 1], DT == GM_F16) << 16);
+      *reinterpret_cast<uint4*>(tile + rl * kTile + cl) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (rows) {
+      uint32_t top = top8(x);
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      float mul;
+      const uint32_t s = block_scale<FMT>(__uint_as_float(top), g, mul);
+      const int j = cl / BL;
+      if (cl % BL == 0) sR[j / 4 * 512 + mx4_atom_byte(rl, j % 4)] = (uint8_t)(r < p.m ? s : 0u);
+      if (r < p.m)
+        *reinterpret_cast<uint32_t*>(p.codes + ((b * (long long)p.m + r) * np + c0 + cl) / 2) =
+            codes8<FMT>(x, s, mul, g);
+    }
+  }
+  __syncthreads();
+
+  // columns 2 lane + 64 (warp & 1), + 1; rows 32 (warp >> 1) .. + 31
+  const int cc = (warp & 1) * 64 + lane * 2, rb = (warp >> 1) * 32;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const long long c = c0 + cc + h;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 32 / BL; ++k) {
+      uint32_t top = 0;
+      float x[BL];
+#pragma unroll
+      for (int i = 0; i < BL; ++i) {
+        const T v = tile[(rb + k * BL + i) * kTile + cc + h];
+        if constexpr (DT == GM_F32) x[i] = v;
+        else x[i] = h16_to_float(v, DT == GM_F16);
+        top = max(top, __float_as_uint(fabsf(x[i])));
+      }
+      float mul;
+      const uint32_t s = block_scale<FMT>(__uint_as_float(top), g, mul);
+      const int j = rb / BL + k;
+      sC[j / 4 * 512 + mx4_atom_byte(cc + h, j % 4)] = (uint8_t)(c < p.n ? s : 0u);
+#pragma unroll
+      for (int q = 0; q < BL / 8; ++q) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = x[q * 8 + e];
+        w[k * (BL / 8) + q] = codes8<FMT>(y, s, mul, g);
+      }
+    }
+    if (c < p.n)
+      *reinterpret_cast<uint4*>(p.codesT + ((b * (long long)p.n + c) * mp + r0 + rb) / 2) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __syncthreads();
+  // atoms [row tile][along the row]: NA per tile
+  for (int i = threadIdx.x; i < NA * 128; i += kThreads) {
+    if (rows)
+      reinterpret_cast<uint32_t*>(p.scales + ((b * p.tiles_m + tm) * p.tiles_n + tn) * NA * 512)[i] =
+          reinterpret_cast<const uint32_t*>(sR)[i];
+    reinterpret_cast<uint32_t*>(p.scalesT + ((b * p.tiles_n + tn) * p.tiles_m + tm) * NA * 512)[i] =
+        reinterpret_cast<const uint32_t*>(sC)[i];
+  }
+}
+
+// ---------------------------------------------------------------------- decoding
+template <int FMT>
+__global__ void __launch_bounds__(kThreads) k_mx4_dequant(int m, int n, long long tiles_m,
+                                                          const uint8_t* __restrict__ codes,
+                                                          const uint8_t* __restrict__ scales,
+                                                          const float* __restrict__ gscale, void* out,
+                                                          int odt, int vec, long long spans) {
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const long long r = blockIdx.x / spans * 8 + (threadIdx.x >> 5);
+  if (r >= m) return;
+  const long long c0 = blockIdx.x % spans * kRowSpan;
+  const long long np = mx4_padded(n), atoms = mx4_atoms(n, FMT);
+  const uint8_t* sc = scales + ((b * tiles_m + r / 128) * atoms) * 512 + mx4_atom_byte((int)(r % 128), 0);
+  const float gs = FMT == GM_NV4 ? gscale[b] : 1.f;
+#pragma unroll
+  for (int u = 0; u < kRowSpan / 256; ++u) {
+    const long long c = c0 + u * 256 + lane * 8;
+    if (c >= n) continue;
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + ((b * (long long)m + r) * np + c) / 2);
+    const long long j = c / mx4_block(FMT);
+    const uint32_t sb = sc[j / 4 * 512 + j % 4];
+    const float s = FMT == GM_MX4 ? e8m0_value(sb) : e4m3_value(sb);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] = __fmul_rn(e2m1_value((w >> (4 * e)) & 15u), s);
+      if constexpr (FMT == GM_NV4) v[e] = __fmul_rn(v[e], gs);
+    }
+    const long long at = (b * (long long)m + r) * n + c;
+    if (vec && c + 8 <= n) {
+      store4_from_float(out, at, odt, make_float4(v[0], v[1], v[2], v[3]));
+      store4_from_float(out, at + 4, odt, make_float4(v[4], v[5], v[6], v[7]));
+    } else {
+      for (int e = 0; e < 8; ++e)
+        if (c + e < n) store_from_float(out, at + e, odt, v[e]);
+    }
+  }
+}
+
+template <int DT, int FMT>
+cudaError_t quant_t(int B, const QuantParams& p, cudaStream_t s) {
+  if constexpr (FMT == GM_NV4) {
+    cudaError_t e = cudaMemsetAsync(p.gscale, 0, (size_t)B * 4, s);
+    if (e != cudaSuccess) return e;
+    const long long items = cdivll(p.n, 8) * p.m;
+    const long long want = cdivll(8LL * sm_count(), B);
+    const int gx = (int)(cdivll(items, kThreads) < want ? cdivll(items, kThreads) : want);
+    k_mx4_top<DT><<<dim3(gx, B), kThreads, 0, s>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (p.codesT) {
+    constexpr size_t bytes = (size_t)kTile * kTile * kElem<DT>;
+    if constexpr (DT == GM_F32) {
+      static DeviceOnce once;
+      const cudaError_t e = smem_attr_once(once, k_mx4_tile<DT, FMT>, bytes);
+      if (e != cudaSuccess) return e;
+    }
+    k_mx4_tile<DT, FMT><<<dim3((unsigned)(p.tiles_m * p.tiles_n), B), kThreads, bytes, s>>>(p);
+  } else {
+    const long long spans = cdivll(mx4_padded(p.n), kRowSpan);
+    k_mx4_rows<DT, FMT><<<dim3((unsigned)(p.tiles_m * 16 * spans), B), kThreads, 0, s>>>(p, spans);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_quant(int B, int m, int n, const void* X, int xdt, long long ldx, long long xbs,
+                             int fmt, float* gscale, uint8_t* codes, uint8_t* scales, uint8_t* codesT,
+                             uint8_t* scalesT, cudaStream_t s) {
+  const int es = xdt == GM_F32 ? 4 : 2;
+  QuantParams p{};
+  p.m = m; p.n = n;
+  p.X = X; p.ldx = ldx; p.xbs = xbs;
+  p.vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && ldx * es % 16 == 0 && (B == 1 || xbs * es % 16 == 0);
+  p.gscale = gscale;
+  p.codes = codes; p.scales = scales; p.codesT = codesT; p.scalesT = scalesT;
+  p.tiles_m = cdivll(m, kTile);
+  p.tiles_n = cdivll(n, kTile);
+  switch (xdt * 2 + fmt) {
+    case GM_F32 * 2 + GM_MX4: return quant_t<GM_F32, GM_MX4>(B, p, s);
+    case GM_F32 * 2 + GM_NV4: return quant_t<GM_F32, GM_NV4>(B, p, s);
+    case GM_BF16 * 2 + GM_MX4: return quant_t<GM_BF16, GM_MX4>(B, p, s);
+    case GM_BF16 * 2 + GM_NV4: return quant_t<GM_BF16, GM_NV4>(B, p, s);
+    case GM_F16 * 2 + GM_MX4: return quant_t<GM_F16, GM_MX4>(B, p, s);
+    case GM_F16 * 2 + GM_NV4: return quant_t<GM_F16, GM_NV4>(B, p, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_mx4_dequant(int B, int m, int n, int fmt, const uint8_t* codes, const uint8_t* scales,
+                               const float* gscale, void* out, int odt, cudaStream_t s) {
+  const long long spans = cdivll(n, kRowSpan), tiles_m = cdivll(m, kTile);
+  const dim3 grid((unsigned)(cdivll(m, 8) * spans), B);
+  const int vec = n % 4 == 0;
+  if (fmt == GM_MX4)
+    k_mx4_dequant<GM_MX4><<<grid, kThreads, 0, s>>>(m, n, tiles_m, codes, scales, gscale, out, odt, vec, spans);
+  else
+    k_mx4_dequant<GM_NV4><<<grid, kThreads, 0, s>>>(m, n, tiles_m, codes, scales, gscale, out, odt, vec, spans);
+  return cudaGetLastError();
+}
+
+}  // namespace gm

@@ -30,6 +30,7 @@ GM_OK, GM_E_ARG, GM_E_CUDA, GM_E_NONFINITE, GM_E_WORKSPACE, GM_E_UNSUPPORTED, GM
 GM_F32, GM_BF16, GM_F16 = 0, 1, 2
 GM_NS_STANDARD, GM_NS_GRAM = 0, 1
 GM_OP_MOMENTUM_POWERIT, GM_OP_NEWTON_SCHULZ, GM_OP_GRAM_NS, GM_OP_GRASP_STEP = 1, 2, 3, 4
+GM_MX4, GM_NV4 = 0, 1
 GRID_BLOCK = 128
 
 _DT = {torch.float32: GM_F32, torch.bfloat16: GM_BF16, torch.float16: GM_F16}
@@ -123,6 +124,14 @@ _sig("gm_grad_norm", c_int, [c_int, vp, ctypes.c_double, vp, vp, vp, vp, c_size_
 _sig("gm_adamw_step", c_int, [c_int, vp, c_int, c_int, c_int, ctypes.POINTER(AdamWParams), vp, vp, vp, vp])
 _sig("gm_adamw_begin", c_int, [ctypes.POINTER(AdamWParams), vp, vp, vp, vp])
 _sig("gm_adamw_apply", c_int, [c_int, vp, c_int, c_int, c_int, ctypes.POINTER(AdamWParams), vp, vp])
+_sig("gm_mx4_codes_bytes", c_size_t, [c_int, c_int, c_int])
+_sig("gm_mx4_scales_bytes", c_size_t, [c_int, c_int, c_int, c_int])
+_sig("gm_mx4_quant", c_int, [c_int, c_int, c_int, vp, c_int, ctypes.c_int64, ctypes.c_int64, c_int,
+                             vp, vp, vp, vp, vp, vp])
+_sig("gm_mx4_dequant", c_int, [c_int, c_int, c_int, c_int, vp, vp, vp, vp, c_int, vp])
+_sig("gm_mx4_matmul_workspace_bytes", c_size_t, [c_int, c_int, c_int, c_int])
+_sig("gm_mx4_matmul", c_int, [c_int, c_int, c_int, c_int, c_int, vp, vp, vp, vp, vp, vp, vp, c_int,
+                              c_int, vp, c_size_t, vp])
 _sig("gm_adamw_unpack8", c_int, [c_int, vp, vp])
 
 
@@ -935,3 +944,168 @@ class AdamWStep:
                 part = np.ascontiguousarray(table[at])
                 _check(lib.gm_adamw_apply(len(at), part.ctypes.data, *key, ctypes.byref(prm),
                                           _ptr(state.scratch), s), "gm_adamw_apply")
+
+
+# ------------------------------------------------ microscaled 4-bit operands
+
+MX4_BLOCK = {GM_MX4: 32, GM_NV4: 16}
+
+
+def _mx4_padded(cols):
+    return -(-cols // 128) * 128
+
+
+@dataclass
+class Mx4:
+    """B matrices of ``rows`` x ``cols`` as microscaled 4-bit values along their rows
+    (GM_MX4: blocks of 32, power-of-two scales; GM_NV4: blocks of 16, e4m3 scales and
+    ``gscale`` [B]). With Kp = cols rounded up to 128: codes uint8 [B, rows, Kp / 2],
+    scales uint8 [B, ceil(rows / 128), Kp / (4 block), 32, 4, 4]."""
+    fmt: int
+    rows: int
+    cols: int
+    codes: torch.Tensor
+    scales: torch.Tensor
+    gscale: torch.Tensor | None = None
+
+    @staticmethod
+    def empty(B, rows, cols, fmt, device=None, gscale=None):
+        """An operand's buffers; ``gscale`` to share another operand's (its transpose's)."""
+        if fmt not in MX4_BLOCK:
+            raise ValueError(f"fmt: GM_MX4 or GM_NV4 expected, got {fmt}")
+        dev = torch.device(device or "cuda")
+        kp = _mx4_padded(cols)
+        if fmt == GM_NV4 and gscale is None:
+            gscale = torch.empty(B, dtype=torch.float32, device=dev)
+        return Mx4(fmt, rows, cols,
+                   torch.empty((B, rows, kp // 2), dtype=torch.uint8, device=dev),
+                   torch.empty((B, -(-rows // 128), kp // (4 * MX4_BLOCK[fmt]), 32, 4, 4),
+                               dtype=torch.uint8, device=dev), gscale)
+
+    def tensors(self):
+        return [self.codes, self.scales] + ([self.gscale] if self.gscale is not None else [])
+
+    def check(self, name="operand"):
+        """Raises ValueError unless the tensors have the operand's layout; returns B."""
+        if self.fmt not in MX4_BLOCK:
+            raise ValueError(f"{name}: fmt: GM_MX4 or GM_NV4 expected, got {self.fmt}")
+        if self.rows < 1 or self.cols < 1 or self.codes.dim() != 3:
+            raise ValueError(f"{name}: codes [B, rows, Kp / 2] of at least one row and column expected")
+        B, kp = self.codes.shape[0], _mx4_padded(self.cols)
+        if tuple(self.codes.shape) != (B, self.rows, kp // 2):
+            raise ValueError(f"{name}: codes: expected shape {(B, self.rows, kp // 2)}, "
+                             f"got {tuple(self.codes.shape)}")
+        want = (B, -(-self.rows // 128), kp // (4 * MX4_BLOCK[self.fmt]), 32, 4, 4)
+        if tuple(self.scales.shape) != want:
+            raise ValueError(f"{name}: scales: expected shape {want}, got {tuple(self.scales.shape)}")
+        parts = [("codes", self.codes, torch.uint8), ("scales", self.scales, torch.uint8)]
+        if self.fmt == GM_NV4:
+            if self.gscale is None or tuple(self.gscale.shape) != (B,):
+                raise ValueError(f"{name}: gscale: expected shape {(B,)}")
+            parts.append(("gscale", self.gscale, torch.float32))
+        for part, t, dt in parts:
+            if t.dtype != dt:
+                raise ValueError(f"{name}: {part}: dtype {t.dtype}, expected {dt}")
+            if t.device != self.codes.device:
+                raise ValueError(f"{name}: {part}: on {t.device}, expected on {self.codes.device}")
+            if not t.is_cuda:
+                raise ValueError(f"{name}: {part}: expected a CUDA tensor")
+            if not t.is_contiguous():
+                raise ValueError(f"{name}: {part}: expected a contiguous tensor")
+        return B
+
+
+def mx4_quant(X, fmt=GM_MX4, rows=True, cols=False, out=None):
+    """Microscaled 4-bit operands of X [B, m, n] (or [m, n]; fp32, bf16 or fp16; rows of
+    any stride, neighbouring elements of a row adjacent): of X itself (``rows``), of its
+    transpose (``cols``, quantised along X's columns), or both from one pass, as a pair.
+    ``out``: the operand (or pair) to write into."""
+    B, m, n = _bmn(X)
+    if X.dtype not in _DT:
+        raise ValueError(f"X: dtype {X.dtype} is not one of {tuple(_DT)}")
+    if fmt not in MX4_BLOCK:
+        raise ValueError(f"fmt: GM_MX4 or GM_NV4 expected, got {fmt}")
+    if not rows and not cols:
+        raise ValueError("rows, cols: one of the two at least")
+    if min(B, m, n) < 1:
+        raise ValueError(f"X: empty ({tuple(X.shape)})")
+    if not X.is_cuda:
+        raise ValueError("X: expected a CUDA tensor")
+    if n > 1 and X.stride(-1) != 1 or m > 1 and X.stride(-2) < n:
+        raise ValueError(f"X: rows of adjacent elements that do not overlap expected, strides {X.stride()}")
+    dev = X.device
+    q = qt = None
+    if out is not None:
+        q, qt = out if rows and cols else (out, None) if rows else (None, out)
+        for o, r, c, name in ((q, m, n, "out"), (qt, n, m, "out (columns)")):
+            if o is None:
+                continue
+            if (o.fmt, o.rows, o.cols) != (fmt, r, c) or o.check(name) != B or o.codes.device != dev:
+                raise ValueError(f"{name}: expected {B} operands of {r} x {c} in format {fmt} on {dev}")
+        if q is not None and qt is not None and fmt == GM_NV4 and q.gscale.data_ptr() != qt.gscale.data_ptr():
+            raise ValueError("out: the two operands of one matrix share one gscale")
+    else:
+        if rows:
+            q = Mx4.empty(B, m, n, fmt, dev)
+        if cols:
+            qt = Mx4.empty(B, n, m, fmt, dev, gscale=q.gscale if rows else None)
+    gs = (q or qt).gscale
+    with _on(dev):
+        _check(lib.gm_mx4_quant(B, m, n, X.data_ptr(), _DT[X.dtype], X.stride(-2) if m > 1 else n,
+                                X.stride(0) if X.dim() == 3 and B > 1 else 0, fmt,
+                                gs.data_ptr() if fmt == GM_NV4 else None,
+                                q.codes.data_ptr() if rows else None, q.scales.data_ptr() if rows else None,
+                                qt.codes.data_ptr() if cols else None,
+                                qt.scales.data_ptr() if cols else None, _stream()), "gm_mx4_quant")
+    return (q, qt) if rows and cols else q if rows else qt
+
+
+def mx4_dequant(q: Mx4, out=None, dtype=torch.float32):
+    """What an operand stands for, [B, rows, cols] in ``dtype`` (gm_mx4_dequant)."""
+    B = q.check("q")
+    dev = q.codes.device
+    if out is None:
+        out = torch.empty((B, q.rows, q.cols), dtype=dtype, device=dev)
+    _expect(out, (B, q.rows, q.cols), tuple(_DT), "out")
+    if out.device != dev:
+        raise ValueError(f"out: expected on {dev}, got {out.device}")
+    with _on(dev):
+        _check(lib.gm_mx4_dequant(B, q.rows, q.cols, q.fmt, _ptr(q.codes), _ptr(q.scales),
+                                  _ptr(q.gscale) if q.fmt == GM_NV4 else None, _ptr(out),
+                                  _DT[out.dtype], _stream()), "gm_mx4_dequant")
+    return out
+
+
+def mx4_matmul(A: Mx4, Bm: Mx4, out_dtype=torch.bfloat16, out=None, accumulate=False, ws=None):
+    """A Bm^T, [B, A.rows, Bm.rows], of two operands with the same columns and format;
+    ``accumulate`` adds to ``out``. A linear layer's forward is mx4_matmul(X, W), its
+    gradients mx4_matmul(dY, W's columns) and mx4_matmul(dY's columns, X's columns)."""
+    B, B2 = A.check("A"), Bm.check("Bm")
+    if (A.fmt, A.cols, B) != (Bm.fmt, Bm.cols, B2):
+        raise ValueError(f"A and Bm: format, columns and batch differ: {(A.fmt, A.cols, B)} "
+                         f"and {(Bm.fmt, Bm.cols, B2)}")
+    dev = A.codes.device
+    if Bm.codes.device != dev:
+        raise ValueError(f"Bm: expected on {dev}, got {Bm.codes.device}")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate: needs out")
+        out = torch.empty((B, A.rows, Bm.rows), dtype=out_dtype, device=dev)
+    _expect(out, (B, A.rows, Bm.rows), tuple(_DT), "out")
+    if out.device != dev:
+        raise ValueError(f"out: expected on {dev}, got {out.device}")
+    nb = int(lib.gm_mx4_matmul_workspace_bytes(B, A.rows, Bm.rows, A.cols))
+    if ws is None:
+        # of this call alone: another stream's or graph's product never shares it
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+    else:
+        _ws_fits(ws, nb)
+        if ws.device != dev:
+            raise ValueError(f"ws: expected on {dev}, got {ws.device}")
+    nv = A.fmt == GM_NV4
+    with _on(dev):
+        _check(lib.gm_mx4_matmul(B, A.rows, Bm.rows, A.cols, A.fmt, _ptr(A.codes), _ptr(A.scales),
+                                 _ptr(A.gscale) if nv else None, _ptr(Bm.codes), _ptr(Bm.scales),
+                                 _ptr(Bm.gscale) if nv else None, _ptr(out), _DT[out.dtype],
+                                 int(bool(accumulate)), _ptr(ws), nb, _stream()), "gm_mx4_matmul")
+    return out

@@ -68,6 +68,7 @@ enum {
 
 typedef enum { GM_F32 = 0, GM_BF16 = 1, GM_F16 = 2 } gm_dtype;
 typedef enum { GM_NS_STANDARD = 0, GM_NS_GRAM = 1 } gm_ns_mode;
+typedef enum { GM_MX4 = 0, GM_NV4 = 1 } gm_mx4_format;
 typedef enum {
   GM_OP_MOMENTUM_POWERIT = 1,
   GM_OP_NEWTON_SCHULZ = 2,
@@ -485,6 +486,66 @@ typedef struct {
   int64_t numel;
 } gm_adamw_state8;
 gm_status gm_adamw_unpack8(int count, const gm_adamw_state8* tensors, gm_stream_t stream);
+
+/*
+ * Microscaled 4-bit floating point: the operands of the next forward and backward
+ * products, made from the fp32 weights that a step updated, from activations and
+ * from their gradients (the OCP Microscaling Formats specification's MXFP4, and
+ * the two-level form with 16-element blocks).
+ * Elements are e2m1: 0, .5, 1, 1.5, 2, 3, 4, 6 with a sign; round to nearest, ties
+ * to the even code, saturating.
+ *   GM_MX4: blocks of 32 along a row; scale byte b stands for 2^(b - 127), b =
+ *     max(floor(log2 max|x|) + 125, 0); a block that holds a NaN or infinity has
+ *     b = 255 (NaN) and zero codes.
+ *   GM_NV4: blocks of 16; one fp32 scale per matrix, gscale = fp32(max|X| / 2688),
+ *     and per block the e4m3 byte nearest to max|x| / (6 gscale); an element stands
+ *     for e2m1 * e4m3 * gscale. A matrix that holds a NaN or infinity has gscale NaN
+ *     and zero codes and scales.
+ *   Codes and scales are those of the exact quotients.
+ * Layout of an operand of `rows` rows and `cols` columns, batch-contiguous, Kp = cols
+ * rounded up to 128, block = 32 or 16:
+ *   codes  uint8 [B][rows][Kp / 2]   element 2i in the low nibble of byte i
+ *   scales uint8 [B][ceil(rows / 128)][Kp / (4 block)][32][4][4]: the scale of row
+ *     r and block j at [r / 128][j / 4][r % 32][r % 128 / 32][j % 4]
+ *   gscale f32 [B] (GM_NV4; ignored, may be NULL, for GM_MX4)
+ * Elements between cols and Kp and their scales are zero, and so are the scales of
+ * rows behind the last. 1 <= B <= 65535; 1 <= rows, cols <= 2^24, their product at
+ * most 2^40; codes and scales 16-byte aligned.
+ */
+size_t gm_mx4_codes_bytes(int B, int rows, int cols);
+size_t gm_mx4_scales_bytes(int B, int rows, int cols, gm_mx4_format fmt);
+
+/*
+ * Quantise B m x n matrices: along rows into codes, scales (an m x n operand), along
+ * columns into codesT, scalesT (the n x m operand of the transpose), or both in one
+ * pass; a pair that is not wanted is NULL. gscale is shared by both (output).
+ *   X of dtype xdt, element (b, i, j) at X[b * batch_stride + i * row_stride + j]
+ *   (strides in elements, non-negative, row_stride >= n unless m = 1); element
+ *   alignment suffices (rows that do not start on 16 bytes are read element by
+ *   element).
+ */
+gm_status gm_mx4_quant(int B, int m, int n, const void* X, gm_dtype xdt, int64_t row_stride,
+                       int64_t batch_stride, gm_mx4_format fmt, float* gscale, uint8_t* codes,
+                       uint8_t* scales, uint8_t* codesT, uint8_t* scalesT, gm_stream_t stream);
+
+/* What an operand stands for: X_out [B][rows][cols] of dtype odt (the product of
+ * the two or three factors in fp32, rounded once to odt). */
+gm_status gm_mx4_dequant(int B, int rows, int cols, gm_mx4_format fmt, const uint8_t* codes,
+                         const uint8_t* scales, const float* gscale, void* X_out, gm_dtype odt,
+                         gm_stream_t stream);
+
+/*
+ * D[b] = A[b] Bm[b]^T (+ D[b] with accumulate = 1): A an M x K operand, Bm an N x K
+ * operand of the same format, D [B][M][N] of dtype ddt (16-byte aligned); sums in
+ * fp32, one rounding. A NaN scale makes its row (A) or column (Bm) NaN.
+ * ws >= gm_mx4_matmul_workspace_bytes(...), 256-byte aligned (may be NULL when that
+ * is 0); calls that overlap on the GPU need their own.
+ */
+size_t gm_mx4_matmul_workspace_bytes(int B, int M, int N, int K);
+gm_status gm_mx4_matmul(int B, int M, int N, int K, gm_mx4_format fmt, const uint8_t* A_codes,
+                        const uint8_t* A_scales, const float* A_gscale, const uint8_t* B_codes,
+                        const uint8_t* B_scales, const float* B_gscale, void* D, gm_dtype ddt,
+                        int accumulate, void* ws, size_t ws_bytes, gm_stream_t stream);
 
 /*
  * Device buffers shared between the processes of one node (CUDA IPC), for the
