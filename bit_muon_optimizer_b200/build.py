@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgmuon.so")
 SOURCES = ["gm_api.cu", "gm_codec.cu", "gm_gemm.cu", "gm_noalloc.cu", "gm_base4.cu", "gm_update.cu",
            "gm_adamw.cu", "gm_mx4.cu", "gm_mx4_gemm.cu"]
-HEADERS = ["gm_common.cuh", "gm_internal.h", "gm_mx4.cuh"]
+HEADERS = ["gm_common.cuh", "gm_internal.h", "gm_mx4.cuh", "gm_tcgen05.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -713,15 +713,10 @@ gm_status gm_mx4_dequant(int B, int rows, int cols, gm_mx4_format fmt, const uin
   return GM_OK;
 }
 
-size_t gm_mx4_matmul_workspace_bytes(int B, int M, int N, int K) {
-  if (!mx4_shape_ok(B, M, K) || !mx4_shape_ok(B, N, K) || !mx4_shape_ok(B, M, N)) return 0;
-  return mx4_matmul_ws_bytes(B, M, N, K);
-}
-
 gm_status gm_mx4_matmul(int B, int M, int N, int K, gm_mx4_format fmt, const uint8_t* A_codes,
                         const uint8_t* A_scales, const float* A_gscale, const uint8_t* B_codes,
                         const uint8_t* B_scales, const float* B_gscale, void* D, gm_dtype ddt,
-                        int accumulate, void* ws, size_t ws_bytes, gm_stream_t stream) {
+                        int accumulate, gm_stream_t stream) {
   GM_CHECK_ARG(mx4_shape_ok(B, M, K) && mx4_shape_ok(B, N, K) && mx4_shape_ok(B, M, N),
                "bad shape B=%d M=%d N=%d K=%d", B, M, N, K);
   GM_CHECK_ARG(mx4_format_ok(fmt) && dtype_ok(ddt), "bad format or dtype");
@@ -731,12 +726,9 @@ gm_status gm_mx4_matmul(int B, int M, int N, int K, gm_mx4_format fmt, const uin
                "device arrays must be 16-byte aligned");
   GM_CHECK_ARG(fmt == GM_MX4 || (A_gscale && B_gscale && aligned(A_gscale, 4) && aligned(B_gscale, 4)),
                "GM_NV4 needs both gscale");
-  const size_t need = mx4_matmul_ws_bytes(B, M, N, K);
-  if (need && (!ws || ws_bytes < need || !aligned256(ws)))
-    return set_error(GM_E_WORKSPACE, "workspace needs %zu bytes, 256-aligned", need);
   GM_DEVICE();
   GM_CUDA(launch_mx4_matmul(B, M, N, K, (int)fmt, A_codes, A_scales, A_gscale, B_codes, B_scales,
-                            B_gscale, D, (int)ddt, accumulate, ws,
+                            B_gscale, D, (int)ddt, accumulate,
                             reinterpret_cast<cudaStream_t>(stream)));
   return GM_OK;
 }

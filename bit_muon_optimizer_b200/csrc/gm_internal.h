@@ -146,10 +146,9 @@ cudaError_t launch_mx4_quant(int B, int m, int n, const void* X, int xdt, long l
                              uint8_t* scalesT, cudaStream_t s);
 cudaError_t launch_mx4_dequant(int B, int m, int n, int fmt, const uint8_t* codes, const uint8_t* scales,
                                const float* gscale, void* out, int odt, cudaStream_t s);
-size_t mx4_matmul_ws_bytes(int B, int M, int N, int K);
 cudaError_t launch_mx4_matmul(int B, int M, int N, int K, int fmt, const uint8_t* a, const uint8_t* as,
                               const float* ag, const uint8_t* b, const uint8_t* bs, const float* bg,
-                              void* D, int ddt, int accumulate, void* ws, cudaStream_t s);
+                              void* D, int ddt, int accumulate, cudaStream_t s);
 
 // Standalone NS input: scale = 1/(|X|_F + eps) per matrix, then the wide
 // 16-bit copy Y = round(scale * X) (transposed when m > n).

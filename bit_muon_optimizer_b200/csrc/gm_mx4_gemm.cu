@@ -1,80 +1,576 @@
-// Products of microscaled 4-bit operands: D[i][j] = sum_k A[i][k] B[j][k] (+ D), the
-// sum in fp32, rounded once to D's type.
+// Products of microscaled 4-bit operands on the tensor cores: D[i][j] =
+// sum_k A[i][k] B[j][k] (+ D), tcgen05.mma kind::mxf4 (GM_MX4) or kind::mxf4nvf4
+// (GM_NV4) on packed e2m1 codes with the block scales in tensor memory, sums in
+// fp32, one rounding to D's type.
+//
+// One kernel, two tile shapes:
+//   CG = 2: a pair of CTAs per 256 x 256 tile (M = 256, N = 256, K = 64 per
+//     instruction), persistent over the tiles. Each CTA loads its 128 rows of A and
+//     128 of the 256 rows of B: per flop the fewest bytes from L2, which bounds the
+//     large products.
+//   CG = 1: one CTA per 128 x 256 tile, and a cluster of up to 8 CTAs that split K and
+//     join their fp32 parts through distributed shared memory in the order of the
+//     ranks (so equal operands give equal bits): for products of few tiles, which
+//     the weight's bytes bound.
+// Roles of a CTA's warps:
+//   warp 0: TMA of A's codes and scales      warp 2: TMA of B's
+//   warp 1: tensor memory; one thread copies a stage's scales to tensor memory
+//           (tcgen05.cp) and issues its MMAs
+//   warps 4..19: epilogue. A warp takes 32 rows and 64 columns into registers at
+//           once, so that the accumulator is free for the next tile before the
+//           results are written.
+// A stage holds 256 columns of K: 128-byte rows of codes in the 128-byte swizzle, and
+// the scale atoms as they lie in memory (512 bytes: 128 rows x 4 blocks), each of
+// which one tcgen05.cp (32 lanes x 128 bits, repeated over the four lane quarters)
+// turns into four columns of tensor memory. The scales of a stage have their own
+// columns, so the copies for a stage never touch what an earlier stage's MMAs read.
+// Every wait is bounded; a timeout is recorded in the device's error word.
+
+#include <cudaTypedefs.h>
+#include <string.h>
 
 #include "gm_common.cuh"
 #include "gm_internal.h"
 #include "gm_mx4.cuh"
+#include "gm_tcgen05.cuh"
 
 namespace gm {
 namespace {
 
+constexpr int kBN = 256;                  // columns of a tile
+constexpr int kStageK = 256;              // columns of K per stage
+constexpr int kStages = 4;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 16;
+constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
+constexpr int kWarpCols = kBN / (kEpiWarps / 4);   // 64 columns of an epilogue warp
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr int kMaxSplit = 8;              // portable cluster size
+
+constexpr uint32_t kABytes = 128 * (kStageK / 2);
+constexpr uint32_t b_bytes(int cg) { return kBN / cg * (kStageK / 2); }
+constexpr uint32_t sf_bytes(int fmt) { return kStageK / (4 * mx4_block(fmt)) * 512; }   // of 128 rows
+constexpr uint32_t stage_bytes(int cg, int fmt) { return kABytes + b_bytes(cg) + 3 * sf_bytes(fmt); }
+constexpr int kPitch = 17;                // staging of ragged stores: 32 rows x 16 columns a warp
+constexpr uint32_t kStageOut = kEpiWarps * 32 * kPitch * 4;
+constexpr uint32_t smem_bytes(int cg, int fmt) {
+  // a CG = 1 stage ring is 195 to 216 KB: there the ragged staging shares it (the
+  // ring is idle by then only when the CTA has one tile), see ragged_base
+  return kStages * stage_bytes(cg, fmt) + (cg == 2 ? kStageOut : 0) + 1024 /* barriers */ + 1024 /* align */;
+}
+static_assert(smem_bytes(1, GM_NV4) <= 227 * 1024 && smem_bytes(2, GM_NV4) <= 227 * 1024, "shared memory");
+constexpr int kPartPitch = kBN + 4;       // fp32 part of a split tile, 16-byte rows without conflicts
+static_assert(128 * kPartPitch * 4 <= kStages * stage_bytes(1, GM_MX4), "a part fits the idle ring");
+
+// Tensor memory columns: accumulator, then per stage the scales of A and of B (4
+// columns per atom of 128 rows).
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t sf_cols(int fmt) { return sf_bytes(fmt) / 128; }   // of 128 rows, one stage
+constexpr uint32_t tmem_sfa(int fmt, int s) { return kBN + s * 3 * sf_cols(fmt); }
+constexpr uint32_t tmem_sfb(int fmt, int s) { return tmem_sfa(fmt, s) + sf_cols(fmt); }
+static_assert(tmem_sfa(GM_NV4, kStages) <= kTmemCols, "tensor memory");
+
 struct ProductParams {
   int M, N, K;
-  const uint8_t *a, *as;
-  const float* ag;
-  const uint8_t *b, *bs;
-  const float* bg;
+  int batch, tiles_m, tiles_n;
+  int split;               // CTAs that share a tile's K (CG = 1)
   void* D;
   int ddt, accumulate;
+  int vec;                 // D's rows start on 32 bytes
+  const float *ag, *bg;    // GM_NV4
+  int32_t* err;
 };
 
-// A 64 x 64 tile of D per CTA, operands decoded into shared memory 64 columns at a
-// time, 4 x 4 outputs a thread.
-template <int FMT>
-__global__ void __launch_bounds__(256) k_mx4_matmul(const ProductParams p) {
-  __shared__ float sA[64][65], sB[64][65];
-  const int bz = blockIdx.z, i0 = blockIdx.x * 64, j0 = blockIdx.y * 64;
-  const long long kp = mx4_padded(p.K), atoms = mx4_atoms(p.K, FMT);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  auto fill = [&](float (&s)[64][65], const uint8_t* codes, const uint8_t* scales, int rows, int r0, long long k0) {
-    for (int i = threadIdx.x; i < 64 * 8; i += 256) {
-      const int r = r0 + i / 8;
-      const long long c = k0 + (i % 8) * 8;
-      uint32_t w = 0, sb = 0;
-      if (r < rows) {
-        w = *reinterpret_cast<const uint32_t*>(codes + (((long long)bz * rows + r) * kp + c) / 2);
-        const long long j = c / mx4_block(FMT);
-        sb = scales[((long long)bz * cdiv(rows, 128) + r / 128) * atoms * 512 + j / 4 * 512 +
-                    mx4_atom_byte(r % 128, (int)(j % 4))];
+// ------------------------------------------------------------ PTX wrappers
+template <int CG>
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar),
+        "r"(x), "r"(y), "r"(z)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar),
+        "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                        int w) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar),
+        "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar),
+        "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+// One scale atom (512 bytes, rows of 16) to four columns of tensor memory, in both
+// CTAs of a pair.
+template <int CG>
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
+  // no swizzle; 128 bytes from one group of eight 16-byte rows to the next
+  const uint64_t d = (uint64_t)((smem >> 4) & 0x3FFF) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+}
+// Instruction descriptor of the block-scaled 4-bit kinds: e2m1 operands, K-major, K =
+// 64; `sf` selects the scale bytes of a 32-bit word to begin with.
+template <int CG, int FMT>
+__host__ __device__ constexpr uint32_t idesc_mx4(uint32_t sf) {
+  return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kBN >> 3) << 17) |
+         ((FMT == GM_MX4 ? 1u : 0u) << 23) | ((uint32_t)(128 * CG >> 7) << 27) | (sf << 29);
+}
+template <int CG, int FMT>
+__device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate) {
+#define GM_UMMA_MX4(GROUP, KIND)                                                                   \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                   \
+               "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d), \
+               "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                     \
+               : "memory")
+  if constexpr (CG == 2 && FMT == GM_MX4) GM_UMMA_MX4("2", "mxf4.block_scale.scale_vec::2X");
+  if constexpr (CG == 2 && FMT == GM_NV4) GM_UMMA_MX4("2", "mxf4nvf4.block_scale.scale_vec::4X");
+  if constexpr (CG == 1 && FMT == GM_MX4) GM_UMMA_MX4("1", "mxf4.block_scale.scale_vec::2X");
+  if constexpr (CG == 1 && FMT == GM_NV4) GM_UMMA_MX4("1", "mxf4nvf4.block_scale.scale_vec::4X");
+#undef GM_UMMA_MX4
+}
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (CG == 2)
+    umma_commit_pair(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// 64 columns of 32 lanes of tensor memory.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+  uint32_t r[64];
+#pragma unroll
+  for (int h = 0; h < 4; ++h)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[16 * h]), "=r"(r[16 * h + 1]), "=r"(r[16 * h + 2]), "=r"(r[16 * h + 3]), "=r"(r[16 * h + 4]),
+          "=r"(r[16 * h + 5]), "=r"(r[16 * h + 6]), "=r"(r[16 * h + 7]), "=r"(r[16 * h + 8]), "=r"(r[16 * h + 9]),
+          "=r"(r[16 * h + 10]), "=r"(r[16 * h + 11]), "=r"(r[16 * h + 12]), "=r"(r[16 * h + 13]),
+          "=r"(r[16 * h + 14]), "=r"(r[16 * h + 15])
+        : "r"(taddr + 16 * h));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// ------------------------------------------------------------------ epilogue
+// 32 bytes of a row: 8 fp32 or 16 16-bit values.
+__device__ __forceinline__ void ld32(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// One warp's 32 rows (a lane each) x 64 columns from column c: whole 32-byte sectors
+// per lane when D's rows are aligned to them, else through shared memory, 16 columns
+// at a time, so that neighbouring lanes write neighbouring elements.
+__device__ __forceinline__ void store_warp(const ProductParams& p, float (&v)[64], int bz, int row0, int c,
+                                           int lane, float* stg) {
+  const long long base = (long long)bz * p.M * p.N;
+  const bool f16 = p.ddt == GM_F16;
+  if (p.vec) {
+    const int r = row0 + lane;
+    if (r >= p.M) return;
+    const long long at = base + (long long)r * p.N + c;
+    if (p.ddt == GM_F32) {
+      float* d = static_cast<float*>(p.D) + at;
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        if (c + g * 8 >= p.N) return;
+        uint32_t w[8];
+        if (p.accumulate) {
+          ld32(d + g * 8, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[g * 8 + e] += __uint_as_float(w[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(v[g * 8 + e]);
+        st32(d + g * 8, w);
       }
-      const float f = r < rows ? (FMT == GM_MX4 ? e8m0_value(sb) : e4m3_value(sb)) : 0.f;
-      for (int e = 0; e < 8; ++e) s[i / 8][(i % 8) * 8 + e] = e2m1_value((w >> (4 * e)) & 15u) * f;
+    } else {
+      uint16_t* d = static_cast<uint16_t*>(p.D) + at;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (c + g * 16 >= p.N) return;
+        uint32_t w[8];
+        if (p.accumulate) {
+          ld32(d + g * 16, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[g * 16 + 2 * e] += h16_to_float((uint16_t)(w[e] & 0xFFFFu), f16);
+            v[g * 16 + 2 * e + 1] += h16_to_float((uint16_t)(w[e] >> 16), f16);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          w[e] = (uint32_t)float_to_h16(v[g * 16 + 2 * e], f16) |
+                 ((uint32_t)float_to_h16(v[g * 16 + 2 * e + 1], f16) << 16);
+        st32(d + g * 16, w);
+      }
     }
-  };
-  for (long long k0 = 0; k0 < kp; k0 += 64) {
-    fill(sA, p.a, p.as, p.M, i0, k0);
-    fill(sB, p.b, p.bs, p.N, j0, k0);
-    __syncthreads();
-    for (int k = 0; k < 64; ++k)
-      for (int u = 0; u < 4; ++u)
-        for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(sA[ty + 16 * u][k], sB[tx + 16 * v][k], acc[u][v]);
-    __syncthreads();
+    return;
   }
-  const float alpha = FMT == GM_NV4 ? p.ag[bz] * p.bg[bz] : 1.f;
-  for (int u = 0; u < 4; ++u)
-    for (int v = 0; v < 4; ++v) {
-      const int i = i0 + ty + 16 * u, j = j0 + tx + 16 * v;
-      if (i >= p.M || j >= p.N) continue;
-      const long long at = ((long long)bz * p.M + i) * p.N + j;
-      float d = acc[u][v] * alpha;
-      if (p.accumulate) d += load_as_float(p.D, at, p.ddt);
-      store_from_float(p.D, at, p.ddt, d);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) stg[lane * kPitch + e] = v[g * 16 + e];
+    __syncwarp();
+    const int col = c + g * 16 + (lane & 15);
+    if (col < p.N) {
+#pragma unroll 4
+      for (int rr = lane >> 4; rr < 32; rr += 2) {
+        const int r = row0 + rr;
+        if (r >= p.M) break;
+        const long long at = base + (long long)r * p.N + col;
+        float d = stg[rr * kPitch + (lane & 15)];
+        if (p.accumulate) d += load_as_float(p.D, at, p.ddt);
+        store_from_float(p.D, at, p.ddt, d);
+      }
     }
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+template <int CG, int FMT>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_mx4_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+               const ProductParams p) {
+  constexpr uint32_t kSf = sf_bytes(FMT), kStage = stage_bytes(CG, FMT), kB = b_bytes(CG);
+  constexpr int kAtoms = kSf / 512;
+  extern __shared__ __align__(1024) uint8_t dsm[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
+  uint8_t* after = ring + kStages * kStage;
+  float* stage_out = reinterpret_cast<float*>(CG == 2 ? after : ring);
+  uint64_t* full = reinterpret_cast<uint64_t*>(after + (CG == 2 ? kStageOut : 0));
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;
+  uint64_t* acc_empty = acc_full + 1;
+  uint64_t* drain = acc_empty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* flags = reinterpret_cast<int*>(tmem_slot + 1);
+  volatile int* abort_flag = flags;
+  int* consumed = flags + 1;
+  int* issued = flags + 2;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int group = CG == 2 ? 2 : p.split;                  // CTAs of a cluster
+  const bool leader = CG == 1 || rank == 0;                 // issues MMAs
+  const int cid = blockIdx.x / group, ncl = gridDim.x / group;
+  const int tiles = p.tiles_m * p.tiles_n, total = p.batch * tiles;
+  const int k64 = (int)(mx4_padded(p.K) / 64);              // instructions along K
+  const int nst = cdiv(k64, kStageK / 64);
+  const int st0 = CG == 1 ? (int)((long long)nst * rank / p.split) : 0;
+  const int st1 = CG == 1 ? (int)((long long)nst * (rank + 1) / p.split) : nst;
+  constexpr uint32_t kStageTx = CG * kStage;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    mbar_init(smem_u32(acc_full), 1);
+    mbar_init(smem_u32(acc_empty), CG * kEpiWarps);
+    mbar_init(smem_u32(drain), 1);
+    flags[0] = flags[1] = flags[2] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    prefetch_map(&tmA);
+    prefetch_map(&tmB);
+    prefetch_map(&tmSA);
+    prefetch_map(&tmSB);
+  }
+  if (warp == 1) {
+    if constexpr (CG == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                   "r"(kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                   "r"(kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (group > 1) cluster_sync_all();   // barriers initialised before any signal from another CTA
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto origin = [&](int T, int& bz, int& r0, int& c0) {
+    bz = T / tiles;
+    const int x = T - bz * tiles;
+    r0 = (x % p.tiles_m) * (128 * CG) + (CG == 2 ? (int)rank * 128 : 0);
+    c0 = x / p.tiles_m * kBN;
+  };
+
+  if (warp == 0 || warp == 2) {
+    if (lane == 0) {
+      // ---------------- TMA producers
+      const bool isA = warp == 0;
+      uint32_t g = 0;
+      bool ok = true;
+      for (int T = cid; T < total && ok; T += ncl) {
+        int bz, r0, c0;
+        origin(T, bz, r0, c0);
+        for (int st = st0; st < st1; ++st, ++g) {
+          const int s = (int)(g % kStages);
+          if (!mbar_wait(smem_u32(&empty[s]), ((g / kStages) & 1u) ^ 1u, p.err, abort_flag, kWaitLimitNs)) { ok = false; break; }
+          const uint32_t bar = CG == 2 ? map_to_rank(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
+          const uint32_t a = smem_u32(ring + s * kStage), b = a + kABytes, sa = b + kB, sb = sa + kSf;
+          if (isA) {
+            if (leader) mbar_expect_tx(smem_u32(&full[s]), kStageTx);
+            load_3d<CG>(a, &tmA, bar, st * (kStageK / 2), r0, bz);
+            load_4d<CG>(sa, &tmSA, bar, 0, st * kAtoms, r0 / 128, bz);
+          } else {
+            load_3d<CG>(b, &tmB, bar, st * (kStageK / 2), c0 + (CG == 2 ? (int)rank * 128 : 0), bz);
+            load_4d<CG>(sb, &tmSB, bar, 0, st * kAtoms, c0 / 128, bz);
+          }
+        }
+      }
+      atomicMax(issued, (int)g);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ---------------- MMA issuer
+      uint32_t g = 0;
+      bool ok = true;
+      int it = 0;
+      for (int T = cid; T < total && ok; T += ncl, ++it) {
+        if (!mbar_wait(smem_u32(acc_empty), ((uint32_t)it & 1u) ^ 1u, p.err, abort_flag, kWaitLimitNs)) { ok = false; break; }
+        tc_fence_after();
+        for (int st = st0; st < st1; ++st, ++g) {
+          const int s = (int)(g % kStages);
+          if (!mbar_wait(smem_u32(&full[s]), (g / kStages) & 1u, p.err, abort_flag, kWaitLimitNs)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a = smem_u32(ring + s * kStage), b = a + kABytes, sa = b + kB, sb = sa + kSf;
+          const uint32_t ta = tmem + tmem_sfa(FMT, s), tb = tmem + tmem_sfb(FMT, s);
+#pragma unroll
+          for (int j = 0; j < kAtoms; ++j) {
+            copy_scales<CG>(ta + j * 4, sa + j * 512);
+            // B: [128-row tile][atom] in shared memory, [atom][tile] in tensor memory
+            copy_scales<CG>(tb + j * 8, sb + j * 512);
+            copy_scales<CG>(tb + j * 8 + 4, sb + kSf + j * 512);
+          }
+#pragma unroll
+          for (int kk = 0; kk < kStageK / 64; ++kk) {
+            const int k = st * (kStageK / 64) + kk;
+            if (k >= k64) break;
+            const int j = kk * kAtoms / (kStageK / 64);          // the atom that holds this k
+            const uint32_t sf = FMT == GM_MX4 ? (kk & 1) * 2 : 0;
+            umma_mx4<CG, FMT>(tmem, sdesc(a + kk * 32, 16, 1024), sdesc(b + kk * 32, 16, 1024),
+                              idesc_mx4<CG, FMT>(sf), ta + j * 4, tb + j * 8, (st > st0 || kk) ? 1u : 0u);
+          }
+          commit<CG>(smem_u32(&empty[s]));
+        }
+        if (!ok) break;
+        commit<CG>(smem_u32(acc_full));
+      }
+      *consumed = (int)g;
+      if (!ok) *abort_flag = 1;
+      commit<CG>(smem_u32(drain));       // fires once every MMA issued above has completed
+      mbar_wait(smem_u32(drain), 0, p.err, nullptr, kWaitLimitNs);
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ---------------- epilogue
+    const int q = warp & 3, part = (warp - kEpiWarp0) >> 2;     // lane quarter, 64-column part
+    const uint32_t bar = CG == 2 ? map_to_rank(smem_u32(acc_empty), 0) : smem_u32(acc_empty);
+    int it = 0;
+    for (int T = cid; T < total; T += ncl, ++it) {
+      int bz, r0, c0;
+      origin(T, bz, r0, c0);
+      const float alpha = FMT == GM_NV4 ? p.ag[bz] * p.bg[bz] : 1.f;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(acc_full), (uint32_t)it & 1u, p.err, abort_flag, kWaitLimitNs))) break;
+      tc_fence_after();
+      float v[64];
+      tmem_ld64(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(part * kWarpCols), v);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+      const int c = c0 + part * kWarpCols;
+      if (FMT == GM_NV4 && group == CG) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) v[e] *= alpha;
+      }
+      if (CG == 1 && group > 1) {
+        // this rank's fp32 part of the tile, in the idle ring
+        float* part_row = reinterpret_cast<float*>(ring) + (q * 32 + lane) * kPartPitch + part * kWarpCols;
+        if (r0 + q * 32 + lane < p.M) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            *reinterpret_cast<float4*>(part_row + 4 * e) = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
+      } else if (c < p.N) {
+        store_warp(p, v, bz, r0 + q * 32, c, lane, stage_out + (warp - kEpiWarp0) * 32 * kPitch);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && leader) {
+    // after an abort, let the copies still in flight land
+    for (int g = *consumed; g < *issued; ++g)
+      mbar_wait(smem_u32(&full[g % kStages]), (uint32_t)(g / kStages) & 1u, p.err, nullptr, kWaitLimitNs);
+  }
+  if (group > 1) cluster_sync_all();
+  if (CG == 1 && group > 1) {
+    // join the parts: vector i of the tile's valid rows belongs to rank i mod split
+    int bz, r0, c0;
+    origin(cid, bz, r0, c0);
+    const float alpha = FMT == GM_NV4 ? p.ag[bz] * p.bg[bz] : 1.f;
+    const int rows = min(128, p.M - r0), cols = min(kBN, p.N - c0);
+    const uint32_t mine = smem_u32(ring);
+    uint32_t remote[kMaxSplit];
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r) remote[r] = r < group ? map_to_rank(mine, r) : 0u;
+    for (int i = threadIdx.x * group + (int)rank; i < rows * (kBN / 4); i += kThreads * group) {
+      const int r = i / (kBN / 4), c = i % (kBN / 4) * 4;
+      if (c >= cols) continue;
+      float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < kMaxSplit; ++s) {
+        if (s >= group) break;
+        float4 x;
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                     : "r"(remote[s] + (uint32_t)((r * kPartPitch + c) * 4))
+                     : "memory");
+        o[0] += x.x; o[1] += x.y; o[2] += x.z; o[3] += x.w;
+      }
+      const long long at = ((long long)bz * p.M + r0 + r) * p.N + c0 + c;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (FMT == GM_NV4) o[e] *= alpha;
+        if (p.accumulate && c + e < cols) o[e] += load_as_float(p.D, at + e, p.ddt);
+      }
+      if (p.N % 4 == 0) {
+        store4_from_float(p.D, at, p.ddt, make_float4(o[0], o[1], o[2], o[3]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < cols) store_from_float(p.D, at + e, p.ddt, o[e]);
+      }
+    }
+    cluster_sync_all();   // no CTA leaves while another still reads its part
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (CG == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ host side
+bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Codes [batch][rows][Kp / 2] with 128-byte x box_rows boxes; rows and columns
+// behind the end read as zero.
+bool map_codes(CUtensorMap* m, const uint8_t* base, int batch, int rows, int K, int box_rows) {
+  const cuuint64_t row = (cuuint64_t)mx4_padded(K) / 2;
+  const cuuint64_t dims[3] = {row, (cuuint64_t)rows, (cuuint64_t)batch};
+  const cuuint64_t strides[2] = {row, row * (cuuint64_t)rows};
+  const cuuint32_t box[3] = {kStageK / 2, (cuuint32_t)box_rows, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// Scales [batch][row tile][atom][128 words]: one stage's atoms of `tiles` row tiles.
+bool map_scales(CUtensorMap* m, const uint8_t* base, int batch, int rows, int K, int fmt, int tiles) {
+  const cuuint64_t atoms = (cuuint64_t)mx4_atoms(K, fmt), rt = (cuuint64_t)cdiv(rows, 128);
+  const cuuint64_t dims[4] = {128, atoms, rt, (cuuint64_t)batch};
+  const cuuint64_t strides[3] = {512, atoms * 512, atoms * 512 * rt};
+  const cuuint32_t box[4] = {128, sf_bytes(fmt) / 512, (cuuint32_t)tiles, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, base, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+struct Maps {
+  CUtensorMap A, B, SA, SB;
+};
+
+template <int CG, int FMT>
+cudaError_t launch_t(const Maps& m, const ProductParams& p, cudaStream_t s) {
+  static DeviceOnce once;
+  const cudaError_t e = smem_attr_once(once, k_mx4_gemm<CG, FMT>, smem_bytes(CG, FMT));
+  if (e != cudaSuccess) return e;
+  const int total = p.tiles_m * p.tiles_n * p.batch;
+  const int group = CG == 2 ? 2 : p.split;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(CG == 2 ? 2 * (total < sm_count() / 2 ? total : sm_count() / 2) : total * group));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes(CG, FMT);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)group;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_mx4_gemm<CG, FMT>, m.A, m.B, m.SA, m.SB, p);
 }
 
 }  // namespace
 
-size_t mx4_matmul_ws_bytes(int, int, int, int) { return 0; }
-
 cudaError_t launch_mx4_matmul(int B, int M, int N, int K, int fmt, const uint8_t* a, const uint8_t* as,
                               const float* ag, const uint8_t* b, const uint8_t* bs, const float* bg,
-                              void* D, int ddt, int accumulate, void*, cudaStream_t s) {
-  const ProductParams p{M, N, K, a, as, ag, b, bs, bg, D, ddt, accumulate};
-  const dim3 grid(cdiv(M, 64), cdiv(N, 64), B);
-  if (fmt == GM_MX4) k_mx4_matmul<GM_MX4><<<grid, 256, 0, s>>>(p);
-  else k_mx4_matmul<GM_NV4><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+                              void* D, int ddt, int accumulate, cudaStream_t s) {
+  ProductParams p{};
+  p.M = M; p.N = N; p.K = K;
+  p.batch = B;
+  p.D = D; p.ddt = ddt; p.accumulate = accumulate;
+  const int per = ddt == GM_F32 ? 8 : 16;   // elements of 32 bytes
+  p.vec = N % per == 0 && reinterpret_cast<uintptr_t>(D) % 32 == 0;
+  p.ag = ag; p.bg = bg;
+  p.err = device_error_word();
+  if (!p.err) return cudaErrorUnknown;
+  p.tiles_n = cdiv(N, kBN);
+  const bool pair = (long long)cdiv(M, 256) * p.tiles_n * B >= sm_count() / 4;
+  p.tiles_m = cdiv(M, pair ? 256 : 128);
+  p.split = 1;
+  if (!pair) {
+    const long long tiles = (long long)p.tiles_m * p.tiles_n * B;
+    const int nst = cdiv((int)(mx4_padded(K) / 64), kStageK / 64);
+    while (p.split < kMaxSplit && tiles * p.split * 2 <= sm_count() && nst >= 4 * p.split) p.split *= 2;
+  }
+  Maps m;
+  if (!map_codes(&m.A, a, B, M, K, 128) || !map_codes(&m.B, b, B, N, K, pair ? 128 : 256) ||
+      !map_scales(&m.SA, as, B, M, K, fmt, 1) || !map_scales(&m.SB, bs, B, N, K, fmt, 2))
+    return cudaErrorInvalidValue;
+  if (fmt == GM_MX4) return pair ? launch_t<2, GM_MX4>(m, p, s) : launch_t<1, GM_MX4>(m, p, s);
+  return pair ? launch_t<2, GM_NV4>(m, p, s) : launch_t<1, GM_NV4>(m, p, s);
 }
 
 }  // namespace gm

@@ -129,9 +129,8 @@ _sig("gm_mx4_scales_bytes", c_size_t, [c_int, c_int, c_int, c_int])
 _sig("gm_mx4_quant", c_int, [c_int, c_int, c_int, vp, c_int, ctypes.c_int64, ctypes.c_int64, c_int,
                              vp, vp, vp, vp, vp, vp])
 _sig("gm_mx4_dequant", c_int, [c_int, c_int, c_int, c_int, vp, vp, vp, vp, c_int, vp])
-_sig("gm_mx4_matmul_workspace_bytes", c_size_t, [c_int, c_int, c_int, c_int])
 _sig("gm_mx4_matmul", c_int, [c_int, c_int, c_int, c_int, c_int, vp, vp, vp, vp, vp, vp, vp, c_int,
-                              c_int, vp, c_size_t, vp])
+                              c_int, vp])
 _sig("gm_adamw_unpack8", c_int, [c_int, vp, vp])
 
 
@@ -1076,7 +1075,7 @@ def mx4_dequant(q: Mx4, out=None, dtype=torch.float32):
     return out
 
 
-def mx4_matmul(A: Mx4, Bm: Mx4, out_dtype=torch.bfloat16, out=None, accumulate=False, ws=None):
+def mx4_matmul(A: Mx4, Bm: Mx4, out_dtype=torch.bfloat16, out=None, accumulate=False):
     """A Bm^T, [B, A.rows, Bm.rows], of two operands with the same columns and format;
     ``accumulate`` adds to ``out``. A linear layer's forward is mx4_matmul(X, W), its
     gradients mx4_matmul(dY, W's columns) and mx4_matmul(dY's columns, X's columns)."""
@@ -1094,18 +1093,10 @@ def mx4_matmul(A: Mx4, Bm: Mx4, out_dtype=torch.bfloat16, out=None, accumulate=F
     _expect(out, (B, A.rows, Bm.rows), tuple(_DT), "out")
     if out.device != dev:
         raise ValueError(f"out: expected on {dev}, got {out.device}")
-    nb = int(lib.gm_mx4_matmul_workspace_bytes(B, A.rows, Bm.rows, A.cols))
-    if ws is None:
-        # of this call alone: another stream's or graph's product never shares it
-        ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
-    else:
-        _ws_fits(ws, nb)
-        if ws.device != dev:
-            raise ValueError(f"ws: expected on {dev}, got {ws.device}")
     nv = A.fmt == GM_NV4
     with _on(dev):
         _check(lib.gm_mx4_matmul(B, A.rows, Bm.rows, A.cols, A.fmt, _ptr(A.codes), _ptr(A.scales),
                                  _ptr(A.gscale) if nv else None, _ptr(Bm.codes), _ptr(Bm.scales),
                                  _ptr(Bm.gscale) if nv else None, _ptr(out), _DT[out.dtype],
-                                 int(bool(accumulate)), _ptr(ws), nb, _stream()), "gm_mx4_matmul")
+                                 int(bool(accumulate)), _stream()), "gm_mx4_matmul")
     return out

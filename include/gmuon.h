@@ -537,15 +537,13 @@ gm_status gm_mx4_dequant(int B, int rows, int cols, gm_mx4_format fmt, const uin
 /*
  * D[b] = A[b] Bm[b]^T (+ D[b] with accumulate = 1): A an M x K operand, Bm an N x K
  * operand of the same format, D [B][M][N] of dtype ddt (16-byte aligned); sums in
- * fp32, one rounding. A NaN scale makes its row (A) or column (Bm) NaN.
- * ws >= gm_mx4_matmul_workspace_bytes(...), 256-byte aligned (may be NULL when that
- * is 0); calls that overlap on the GPU need their own.
+ * fp32 in a fixed order, one rounding. A NaN scale makes its row (A) or column (Bm)
+ * NaN. No workspace. A wait that runs out is reported by gm_device_errors().
  */
-size_t gm_mx4_matmul_workspace_bytes(int B, int M, int N, int K);
 gm_status gm_mx4_matmul(int B, int M, int N, int K, gm_mx4_format fmt, const uint8_t* A_codes,
                         const uint8_t* A_scales, const float* A_gscale, const uint8_t* B_codes,
                         const uint8_t* B_scales, const float* B_gscale, void* D, gm_dtype ddt,
-                        int accumulate, void* ws, size_t ws_bytes, gm_stream_t stream);
+                        int accumulate, gm_stream_t stream);
 
 /*
  * Device buffers shared between the processes of one node (CUDA IPC), for the

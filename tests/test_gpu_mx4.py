@@ -197,7 +197,9 @@ def _check_product(gm, A, Bm, got, before=None):
 
 
 SIZES = [(1, 1, 1), (1, 16, 32), (5, 3, 7), (16, 256, 512), (128, 256, 256), (129, 257, 130), (128, 128, 64),
-         (300, 200, 1000), (1, 3584, 2048), (7, 500, 4100), (1000, 773, 771), (64, 64, 16384), (257, 1025, 33)]
+         (300, 200, 1000), (1, 3584, 2048), (7, 500, 4100), (1000, 773, 771), (64, 64, 16384), (257, 1025, 33),
+         # enough tiles for CTA pairs: one tile a pair, several, ragged ends, short and odd K
+         (2048, 1500, 200), (1700, 2053, 771), (4096, 5632, 2048), (5000, 3000, 100), (129, 9500, 640)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -216,7 +218,8 @@ def test_product(cuda_lib, fmt, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("M,N,K", [(3, 5, 7), (128, 256, 256), (130, 300, 1030), (1, 600, 9000), (400, 900, 512)])
+@pytest.mark.parametrize("M,N,K", [(3, 5, 7), (128, 256, 256), (130, 300, 1030), (1, 600, 9000), (400, 900, 512),
+                                   (2500, 1300, 1030), (3000, 6000, 256)])
 def test_product_of_small_multiples_is_exact(cuda_lib, fmt, M, N, K):
     """Entries that are e2m1 numbers, scales all one: every sum is a multiple of 1/4
     below 2^22, so fp32 holds each step and D equals the fp64 product bit for bit."""
@@ -240,27 +243,29 @@ def test_product_of_small_multiples_is_exact(cuda_lib, fmt, M, N, K):
     assert torch.equal(D.cpu().double(), ops[0][1] @ ops[1][1].transpose(-1, -2))
 
 
+@pytest.mark.parametrize("M,pad", [(260, 0), (2600, 1500)])
 @pytest.mark.parametrize("fmt", FMTS)
-def test_product_places_every_scale(cuda_lib, fmt):
+def test_product_places_every_scale(cuda_lib, fmt, M, pad):
     """One non-zero element per row with its own block scale: D shows each scale byte."""
     gm = cuda_lib
     f = _fmt(gm, fmt)
-    M, K = 260, 1024
+    K = 1024
     blk = OM.BLOCK[fmt]
     nb = K // blk
+    N = nb + pad                                                # more columns: CTA pairs
     g = torch.Generator().manual_seed(7)
-    A, Bm = gm.Mx4.empty(1, M, K, f, DEV), gm.Mx4.empty(1, nb, K, f, DEV)
+    A, Bm = gm.Mx4.empty(1, M, K, f, DEV), gm.Mx4.empty(1, N, K, f, DEV)
     codes = torch.zeros(1, M, K, dtype=torch.long)
     codes[..., ::blk] = 2                                       # 1.0 at the head of every block
     byte = torch.randint(100, 150, (1, M, nb), generator=g) if fmt == "mx" else \
         torch.randint(1, 127, (1, M, nb), generator=g)
     A.codes.copy_(OM.pack(codes))
     A.scales.copy_(OM.tile_scales(byte))
-    sel = torch.zeros(1, nb, K, dtype=torch.long)
-    sel[0, torch.arange(nb), torch.arange(nb) * blk] = 2        # row j picks block j
+    sel = torch.zeros(1, N, K, dtype=torch.long)
+    sel[0, torch.arange(N), torch.arange(N) % nb * blk] = 2     # row j picks block j mod nb
     Bm.codes.copy_(OM.pack(sel))
-    sb = torch.randint(100, 150, (1, nb, nb), generator=g) if fmt == "mx" else \
-        torch.randint(1, 127, (1, nb, nb), generator=g)
+    sb = torch.randint(100, 150, (1, N, nb), generator=g) if fmt == "mx" else \
+        torch.randint(1, 127, (1, N, nb), generator=g)
     Bm.scales.copy_(OM.tile_scales(sb))
     if fmt == "nv":
         A.gscale.fill_(1.0)
@@ -273,7 +278,8 @@ def test_product_places_every_scale(cuda_lib, fmt):
 def test_product_batched_accumulated(cuda_lib, fmt):
     gm = cuda_lib
     f = _fmt(gm, fmt)
-    for B, M, N, K in [(3, 40, 70, 200), (2, 130, 260, 300), (5, 1, 256, 4096)]:
+    for B, M, N, K in [(3, 40, 70, 200), (2, 130, 260, 300), (5, 1, 256, 4096), (3, 1000, 1031, 300),
+                       (2, 1100, 1536, 700)]:
         A = gm.mx4_quant(_random((B, M, K), 1).to(DEV), f)
         Bm = gm.mx4_quant(_random((B, N, K), 2, std=0.1).to(DEV), f)
         for dt in (F32, BF16, F16):
@@ -345,7 +351,7 @@ def test_products_on_two_streams_and_in_a_graph(cuda_lib, fmt):
     for o in outs:
         o.zero_()
     torch.cuda.synchronize()
-    for i, g in enumerate(graphs * 2):          # two graphs at a time, each with its own workspace
+    for i, g in enumerate(graphs * 2):          # two graphs at a time
         with torch.cuda.stream(streams[i % 2]):
             g.replay()
     torch.cuda.synchronize()

@@ -58,7 +58,6 @@ def test_sizes():
     assert f.gm_mx4_scales_bytes(2, 129, 130, gm.GM_NV4) == 2 * 2 * 4 * 512
     for B, r, c in [(0, 1, 1), (65536, 1, 1), (1, 0, 1), (1, 1, 0), (1, (1 << 24) + 1, 1), (1, 1 << 24, 1 << 17)]:
         assert f.gm_mx4_codes_bytes(B, r, c) == 0 and f.gm_mx4_scales_bytes(B, r, c, 0) == 0
-        assert f.gm_mx4_matmul_workspace_bytes(B, r, c, 8) == 0
     assert f.gm_mx4_scales_bytes(1, 1, 1, 2) == 0
     q = gm.Mx4.empty(3, 200, 77, gm.GM_NV4, device="cpu")
     assert q.codes.numel() == f.gm_mx4_codes_bytes(3, 200, 77)
@@ -83,17 +82,12 @@ def test_c_refusals():
                dict(out=None), dict(codes=4104), dict(sc=4104), dict(out=4104), dict(gs=None)]:
         assert deq(**kw) == gm.GM_E_ARG, kw
 
-    def mm(B=1, M=4, N=5, K=40, fmt=1, a=ok, sa=ok, ga=ok, b=ok, sb=ok, gb=ok, D=ok, dt=0, acc=0,
-           ws=ok, nb=1 << 40):
-        return gm.lib.gm_mx4_matmul(B, M, N, K, fmt, a, sa, ga, b, sb, gb, D, dt, acc, ws, nb, None)
+    def mm(B=1, M=4, N=5, K=40, fmt=1, a=ok, sa=ok, ga=ok, b=ok, sb=ok, gb=ok, D=ok, dt=0, acc=0):
+        return gm.lib.gm_mx4_matmul(B, M, N, K, fmt, a, sa, ga, b, sb, gb, D, dt, acc, None)
     for kw in [dict(B=0), dict(M=0), dict(N=0), dict(K=0), dict(fmt=3), dict(dt=4), dict(acc=2), dict(a=None),
                dict(sa=None), dict(b=None), dict(sb=None), dict(D=None), dict(a=4104), dict(sb=4104),
                dict(D=4104), dict(ga=None), dict(gb=None), dict(gb=4098)]:
         assert mm(**kw) == gm.GM_E_ARG, kw
-    need = gm.lib.gm_mx4_matmul_workspace_bytes(1, 1, 512, 16384)
-    if need:
-        for kw in [dict(ws=None), dict(nb=need - 1), dict(ws=4096 + 16)]:
-            assert mm(M=1, N=512, K=16384, **kw) == gm.GM_E_WORKSPACE, kw
 
 
 def test_binding_refusals():
