@@ -301,8 +301,8 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Tabl
         float sm = scale_of(tm, 1.0f / kTopM), sv = scale_of(tr, 1.0f / kTopR);
         const float im = __frcp_rn(sm), iv = __frcp_rn(sv);
         // The stored codes are those of m and r in fp64 (each product and sum rounded
-        // singly: true ties occur, r / max r is a quotient of short numbers after the
-        // first step). fp32 decides a code unless its value lies so close to a border
+        // singly, 1 / 448 and 1 / 1.9375 being constants: true ties occur, for m and r
+        // are made of short numbers, and the roundings decide them). fp32 decides a code unless its value lies so close to a border
         // that its error could cross it; then the group is redone in fp64. Errors, u = 2^-24: m is off by 5 u size
         // at most (two products of three roundings, one sum), m / sm by that and by
         // sm's own relative error, 5 u ts / tm, plus a few u; r by 8 u.
@@ -335,8 +335,8 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Tabl
             xm = fmax(xm, fabs(dm[e]));
             xv = fmax(xv, dv[e]);
           }
-          const double dsm = fmax(warp_max(xm) / 448.0, pow2d(-126));
-          const double dsv = fmax(sqrt(warp_max(xv)) / 1.9375, pow2d(-126));
+          const double dsm = fmax(__dmul_rn(warp_max(xm), 1.0 / 448.0), pow2d(-126));
+          const double dsv = fmax(__dmul_rn(sqrt(warp_max(xv)), 1.0 / 1.9375), pow2d(-126));
           wm = wv = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {

@@ -433,7 +433,8 @@ gm_status gm_grad_norm(int count, const gm_grad* grads, double max_norm, float* 
  *       fp32 gets code 1 at least.
  *     The step uses the new m and v before they are rounded to 8 bits, and the codes
  *     are the nearest ones (ties to even) to m / sm and sqrt(v) / sv in fp64, each
- *     operation above rounded singly. A group that a NaN or infinity enters (or a
+ *     operation above rounded singly (/ 448 and / 1.9375 as products with the
+ *     rounded reciprocal). A group that a NaN or infinity enters (or a
  *     g^2 past fp32's range) becomes NaN as a whole.
  *     No two entries may overlap. All-zero codes and scales are the zero state.
  *   step int64 [1] (device): completed steps, incremented by this one; scratch:

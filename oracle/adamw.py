@@ -52,8 +52,10 @@ def encode8(m, v):
     n = m.numel()
     mg, vg = _groups(m.double()), _groups(v.double())
     rg = root(vg)
-    sm = (mg.abs().amax(1) / 448).clamp_min(SCALE_FLOOR)
-    sv = (rg.amax(1) / 1.9375).clamp_min(SCALE_FLOOR)
+    # products with the reciprocals, as the definition has it: at a true tie of a
+    # code's quotient the last place of the scale decides
+    sm = (mg.abs().amax(1) * (1 / 448)).clamp_min(SCALE_FLOOR)
+    sv = (rg.amax(1) * (1 / 1.9375)).clamp_min(SCALE_FLOOR)
     cm = nearest((mg / sm[:, None]).abs(), m_levels()) + 128 * (mg < 0).long()
     cv = nearest(rg / sv[:, None], root_levels())
     cv = torch.maximum(cv, (vg.float() > 0).long())
