@@ -128,16 +128,17 @@ __device__ __forceinline__ void e4m3x4_to_float(uint32_t w, float (&o)[4]) {
 }
 // Exponents 0..15 of the 4 + 4 bit float are fp32's own lowest ones (a value x is
 // kept as the fp32 number x 2^-112): code << 19 are that number's bits, subnormals
-// included, and rounding to nearest even is on the bits.
+// included, and rounding is on the bits.
 __device__ __forceinline__ float root_value(uint32_t code) {
   return __fmul_rn(__uint_as_float(code << 19), 5.192296858534828e33f);   // 2^112
 }
 __device__ __forceinline__ uint32_t root_bits(float y) {
   return __float_as_uint(__fmul_rn(y, 1.925929944387236e-34f));           // 2^-112
 }
-__device__ __forceinline__ uint32_t root_code(uint32_t bits, float v) {
-  const uint32_t c = min((bits + 0x3FFFFu + ((bits >> 19) & 1u)) >> 19, 255u);
-  return v > 0.f ? max(c, 1u) : c;
+__device__ __forceinline__ float approx_sqrt(float x) {   // 2^-23
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // Both codes from fp64 values (round to nearest, ties to even).
@@ -217,6 +218,42 @@ struct Consts {
 constexpr int kUnroll = 2;                                    // groups of a warp in flight
 constexpr int kChunk = kWarps * kUnroll * kGroup8;
 
+// The codes and scales of a group in fp64, four elements a lane (kept out of line:
+// one group in a few hundred comes here).
+struct Codes8 {
+  uint32_t m, v;
+  float sm, sv;
+};
+struct Quad {
+  float x[4];
+};
+__device__ __noinline__ Codes8 exact_codes_of(const Consts& k, double c, Quad g, Quad mo, Quad ro, float ms, float vs) {
+  double dm[4], dv[4], xm = 0.0, xv = 0.0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const double gd = __dmul_rn((double)g.x[e], c);
+    const double rd = (double)ro.x[e] * (double)vs, md = (double)mo.x[e] * (double)ms;
+    dm[e] = __dadd_rn(__dmul_rn(k.db1, md), __dmul_rn(k.dob1, gd));
+    dv[e] = __dadd_rn(__dmul_rn(k.db2, __dmul_rn(rd, rd)), __dmul_rn(k.dob2, __dmul_rn(gd, gd)));
+    xm = fmax(xm, fabs(dm[e]));
+    xv = fmax(xv, dv[e]);
+  }
+  const double dsm = fmax(__dmul_rn(warp_max(xm), 1.0 / 448.0), pow2d(-126));
+  const double dsv = fmax(__dmul_rn(sqrt(warp_max(xv)), 1.0 / 1.9375), pow2d(-126));
+  Codes8 o{0, 0, (float)dsm, (float)dsv};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    o.m |= e4m3_from_double(dm[e] / dsm) << (8 * e);
+    o.v |= root_from_double(sqrt(dv[e]) / dsv, dv[e]) << (8 * e);
+  }
+  return o;
+}
+__device__ __forceinline__ Codes8 exact_codes(const Consts& k, double c, const float (&g)[4], const float (&mo)[4],
+                                              const float (&ro)[4], float ms, float vs) {
+  return exact_codes_of(k, c, Quad{g[0], g[1], g[2], g[3]}, Quad{mo[0], mo[1], mo[2], mo[3]},
+                        Quad{ro[0], ro[1], ro[2], ro[3]}, ms, vs);
+}
+
 template <int PDT, int GDT, int BITS>
 __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Table t, const Consts k,
                                                     const Coef* __restrict__ coef) {
@@ -271,14 +308,19 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Tabl
       float size[4], r[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float gc = __fmul_rn(g[u][e], c);
-        const float a = __fmul_rn(k.b1, m[u][e]), b = __fmul_rn(k.ob1, gc);
+        const float gc = g[u][e] * c;
+        const float a = k.b1 * m[u][e], b = k.ob1 * gc;
         size[e] = fabsf(a) + fabsf(b);
-        m[u][e] = __fadd_rn(a, b);
-        v[u][e] = __fadd_rn(__fmul_rn(k.b2, v[u][e]), __fmul_rn(__fmul_rn(gc, gc), k.ob2));
-        r[e] = __fsqrt_rn(v[u][e]);
-        const float x = __fdiv_rn(m[u][e], __fadd_rn(__fmul_rn(r[e], root), k.eps));
-        p[u][e] = __fsub_rn(__fmul_rn(p[u][e], decay), __fmul_rn(x, scale));
+        m[u][e] = a + b;
+        v[u][e] = fmaf(k.b2, v[u][e], gc * gc * k.ob2);
+        if constexpr (BITS == 32) {
+          r[e] = __fsqrt_rn(v[u][e]);
+          p[u][e] = fmaf(p[u][e], decay, -__fdiv_rn(m[u][e], fmaf(r[e], root, k.eps)) * scale);
+        } else {
+          // 2^-22 of an update: IEEE roots and quotients would bound this kernel by its issue rate
+          r[e] = approx_sqrt(v[u][e]);
+          p[u][e] = fmaf(p[u][e], decay, -__fdividef(m[u][e], fmaf(r[e], root, k.eps)) * scale);
+        }
       }
       store4(E.p, i, n, vec, PDT, p[u]);
       if (E.copy) store4(E.copy, i, n, vec, k.cdt, p[u]);
@@ -288,63 +330,50 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Tabl
       } else {
         if (left <= u * kGroup8) continue;   // the whole warp
         // |x| as unsigned bits orders like the values; a NaN is above all of them
-        uint32_t am = 0, as = 0, ar = 0;
+        uint32_t am = 0, ar = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           am = max(am, __float_as_uint(fabsf(m[u][e])));
-          as = max(as, __float_as_uint(size[e]));
           ar = max(ar, __float_as_uint(fabsf(r[e])));
         }
         const float tm = __uint_as_float(__reduce_max_sync(0xffffffffu, am));
-        const float ts = __uint_as_float(__reduce_max_sync(0xffffffffu, as));
         const float tr = __uint_as_float(__reduce_max_sync(0xffffffffu, ar));
         float sm = scale_of(tm, 1.0f / kTopM), sv = scale_of(tr, 1.0f / kTopR);
         const float im = __frcp_rn(sm), iv = __frcp_rn(sv);
         // The stored codes are those of m and r in fp64 (each product and sum rounded
         // singly, 1 / 448 and 1 / 1.9375 being constants: true ties occur, for m and r
-        // are made of short numbers, and the roundings decide them). fp32 decides a code unless its value lies so close to a border
-        // that its error could cross it; then the group is redone in fp64. Errors, u = 2^-24: m is off by 5 u size
-        // at most (two products of three roundings, one sum), m / sm by that and by
-        // sm's own relative error, 5 u ts / tm, plus a few u; r by 8 u.
-        const float rho = tm > 0.f ? __fdividef(ts, tm) + 1.f : 0.f;
+        // are made of short numbers, and the roundings decide them). fp32 decides a code
+        // unless its value lies so close to a border that its error could cross it;
+        // then the group is redone in fp64. Errors, u = 2^-24: m is off by 5 u size
+        // at most (two products of three roundings, one sum), and m / sm by that and by
+        // sm's relative error, 5 u size / tm of the top element plus a few u: size up
+        // to 3 tm is allowed for, a group with more is redone. r is off by 10 u.
         // Near fp32's subnormals these bounds do not hold: 2^-90 and 2^-40 keep the
         // smallest element that gets a code (2^-18 of the top) and its square above them.
         bool near = (tm > 0.f && tm < 8.1e-28f) || (tr > 0.f && tr < 9.1e-13f);
-        uint32_t wm = 0, wv = 0;
+        const float wide = 3.f * tm, w21 = im * 4.76837158e-7f;   // 2^-21
+        float lo[4], hi[4];
+        uint32_t cv[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float y = __fmul_rn(m[u][e], im);
-          const float d = (size[e] + fabsf(m[u][e]) * rho) * (im * 4.76837158e-7f);   // 2^-21
-          const uint32_t q = e4m3x2(y - d, y + d);
-          near |= (q & 255u) != (q >> 8);
-          wm |= (q & 255u) << (8 * e);
-          const uint32_t bits = root_bits(__fmul_rn(r[e], iv));
-          const uint32_t low = bits & 0x7FFFFu;
-          near |= low - (0x40000u - 32u) <= 64u;
-          wv |= root_code(bits, v[u][e]) << (8 * e);
+          near |= size[e] > wide;
+          const float d = fmaf(fabsf(m[u][e]), 4.f, size[e]) * w21;
+          lo[e] = fmaf(m[u][e], im, -d);
+          hi[e] = fmaf(m[u][e], im, d);
+          // the code's border is at a set bit 18 with zeros below; +-32 around it
+          const uint32_t bits = root_bits(r[e] * iv) + 0x40000u + 32u;
+          near |= (bits & 0x7FFFFu) <= 64u;
+          cv[e] = max(bits >> 19, min(__float_as_uint(v[u][e]), 1u));
         }
+        uint32_t wm = e4m3x2(lo[0], lo[1]) | (e4m3x2(lo[2], lo[3]) << 16);
+        near |= wm != (e4m3x2(hi[0], hi[1]) | (e4m3x2(hi[2], hi[3]) << 16));
+        uint32_t wv = cv[0] | (cv[1] << 8) | (cv[2] << 16) | (cv[3] << 24);
         if (__any_sync(0xffffffffu, near) && tm <= 3.402823466e38f && tr <= 3.402823466e38f) {
-          const double dc = coef->c;
-          double dm[4], dv[4], xm = 0.0, xv = 0.0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const double gd = __dmul_rn((double)g[u][e], dc);
-            const double rd = (double)ro[e] * (double)vs[u], md = (double)mo[e] * (double)ms[u];
-            dm[e] = __dadd_rn(__dmul_rn(k.db1, md), __dmul_rn(k.dob1, gd));
-            dv[e] = __dadd_rn(__dmul_rn(k.db2, __dmul_rn(rd, rd)), __dmul_rn(k.dob2, __dmul_rn(gd, gd)));
-            xm = fmax(xm, fabs(dm[e]));
-            xv = fmax(xv, dv[e]);
-          }
-          const double dsm = fmax(__dmul_rn(warp_max(xm), 1.0 / 448.0), pow2d(-126));
-          const double dsv = fmax(__dmul_rn(sqrt(warp_max(xv)), 1.0 / 1.9375), pow2d(-126));
-          wm = wv = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            wm |= e4m3_from_double(dm[e] / dsm) << (8 * e);
-            wv |= root_from_double(sqrt(dv[e]) / dsv, dv[e]) << (8 * e);
-          }
-          sm = (float)dsm;
-          sv = (float)dsv;
+          const Codes8 x = exact_codes(k, coef->c, g[u], mo, ro, ms[u], vs[u]);
+          wm = x.m;
+          wv = x.v;
+          sm = x.sm;
+          sv = x.sv;
         }
         store4_codes(static_cast<uint8_t*>(E.m), i, n, vec, wm);
         store4_codes(static_cast<uint8_t*>(E.v), i, n, vec, wv);

@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTile = 128;
+constexpr int kRowSpan = 1024;   // elements of a row that a warp takes at a time
 
 // Eight consecutive elements from column c of a row of n (zeros behind its end).
 template <int DT>
@@ -87,6 +88,15 @@ __device__ __forceinline__ MatrixScale matrix_scale(const float* gscale, int b) 
   return g;
 }
 
+// e4m3 nearest to top / (6 gs), in fp64 (out of line: it runs for one block in 10^4).
+__device__ __noinline__ uint32_t exact_scale(float top, float gs) {
+  // 3 fraction bits, exponents from -6, at most 448
+  const double t = (double)top / (6.0 * (double)gs);
+  const int e = max((__double2hiint(t) >> 20) - 1023, -6);
+  const int k = (int)rint(fmin(t, 449.0) * __hiloint2double((3 - e + 1023) << 20, 0));
+  return min((uint32_t)(((e + 6) << 3) + k), 126u);
+}
+
 // The scale byte of a block whose largest magnitude is `top` (a NaN's bits lie
 // above every number's), and what its elements are multiplied by.
 template <int FMT>
@@ -111,22 +121,30 @@ __device__ __forceinline__ uint32_t block_scale(float top, const MatrixScale& g,
       b = q & 255u;
       sure = b == (q >> 8);
     }
-    if (!sure) {
-      // rn to 3 fraction bits, exponents from -6, at most 448
-      const double t = (double)top / (6.0 * (double)g.gs);
-      const int e = max((__double2hiint(t) >> 20) - 1023, -6);
-      const int k = (int)rint(fmin(t, 449.0) * __hiloint2double((3 - e + 1023) << 20, 0));
-      b = min((uint32_t)(((e + 6) << 3) + k), 126u);
-    }
-    if (b) mul = __fdiv_rn(1.0f, e4m3_value(b) * g.gs);
+    if (!sure) b = exact_scale(top, g.gs);
+    // within 2^-22 of 1 / (sb gs); where it leaves fp32's range the codes are exact_codes'
+    if (b) mul = __fdividef(1.0f, e4m3_value(b) * g.gs);
     return b;
   }
 }
 
-__device__ __forceinline__ uint32_t e2m1_exact(float x, double s) {
-  const double a = fabs((double)x) / s;
-  const uint32_t c = (a > 0.25) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0);
-  return c | (x < 0.f ? 8u : 0u);
+// Codes of eight elements under sb gs: |x| against border * sb * gs, a product of at
+// most 31 bits, exact in fp64.
+struct Eight {
+  float x[8];
+};
+__device__ __noinline__ uint32_t exact_codes(Eight v, float sb, float gs) {
+  const double s = (double)sb * (double)gs;
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const double a = fabs((double)v.x[e]);
+    uint32_t c = (a > 0.25 * s) + (a >= 0.75 * s) + (a > 1.25 * s) + (a >= 1.75 * s) + (a > 2.5 * s) +
+                 (a >= 3.5 * s) + (a > 5.0 * s);
+    if (v.x[e] < 0.f) c |= 8u;
+    w |= c << (4 * e);
+  }
+  return w;
 }
 
 // Codes of eight elements of one block.
@@ -141,18 +159,15 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8], uint32_t b, floa
   } else {
     if (b == 0u) return 0u;
     float z[8];
+    const float below = mul * kBelow, above = mul * kAbove;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      y[e] = x[e] * (mul * kBelow);
-      z[e] = x[e] * (mul * kAbove);
+      y[e] = x[e] * below;
+      z[e] = x[e] * above;
     }
     uint32_t w = e2m1x8(y);
-    if (w != e2m1x8(z) || g.exact) {
-      const double s = (double)e4m3_value(b) * (double)g.gs;
-      w = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w |= e2m1_exact(x[e], s) << (4 * e);
-    }
+    if (w != e2m1x8(z) || g.exact)
+      w = exact_codes(Eight{x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]}, e4m3_value(b), g.gs);
     return w;
   }
 }
@@ -187,15 +202,19 @@ constexpr int kElem = DT == GM_F32 ? 4 : 2;
 // maximum); an infinity or a NaN leaves a NaN.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_mx4_top(const QuantParams p) {
-  const int b = blockIdx.y;
-  const long long c8 = (p.n + 7) / 8, items = c8 * p.m;
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
   uint32_t top = 0;
-  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < items;
-       i += (long long)gridDim.x * kThreads) {
-    const long long r = i / c8, c = (i - r * c8) * 8;
-    float x[8];
-    load8<DT>(row_ptr(p, b, r, kElem<DT>), c, p.n, p.vec != 0, x);
-    top = max(top, top8(x));
+  // a warp takes pieces of 1024 elements of a row
+  const long long spans = cdivll(p.n, kRowSpan), items = spans * p.m;
+  for (long long i = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < items;
+       i += (long long)gridDim.x * (kThreads / 32)) {
+    const long long r = i / spans, c0 = (i - r * spans) * kRowSpan;
+    const void* row = row_ptr(p, b, r, kElem<DT>);
+    float x[kRowSpan / 256][8];
+#pragma unroll
+    for (int u = 0; u < kRowSpan / 256; ++u) load8<DT>(row, c0 + u * 256 + lane * 8, p.n, p.vec != 0, x[u]);
+#pragma unroll
+    for (int u = 0; u < kRowSpan / 256; ++u) top = max(top, top8(x[u]));
   }
   top = __reduce_max_sync(0xffffffffu, top);
   __shared__ uint32_t part[kThreads / 32];
@@ -214,7 +233,6 @@ __global__ void __launch_bounds__(kThreads) k_mx4_top(const QuantParams p) {
 // block's maximum is shared by 4 (GM_MX4) or 2 lanes, a word of four scale bytes
 // gathered from 16 or 8. A CTA takes 8 rows and kRowSpan columns. Rows of the last
 // 128-row tile behind m get zero scales.
-constexpr int kRowSpan = 1024;
 template <int DT, int FMT>
 __global__ void __launch_bounds__(kThreads) k_mx4_rows(const QuantParams p, long long spans) {
   const int b = blockIdx.y, lane = threadIdx.x & 31;
@@ -368,27 +386,35 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequant(int m, int n, long lon
   const long long np = mx4_padded(n), atoms = mx4_atoms(n, FMT);
   const uint8_t* sc = scales + ((b * tiles_m + r / 128) * atoms) * 512 + mx4_atom_byte((int)(r % 128), 0);
   const float gs = FMT == GM_NV4 ? gscale[b] : 1.f;
-#pragma unroll
-  for (int u = 0; u < kRowSpan / 256; ++u) {
-    const long long c = c0 + u * 256 + lane * 8;
-    if (c >= n) continue;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + ((b * (long long)m + r) * np + c) / 2);
+  const uint8_t* row = codes + (b * (long long)m + r) * (np / 2);
+  const long long at = (b * (long long)m + r) * n;
+  auto factor = [&](long long c) {
     const long long j = c / mx4_block(FMT);
     const uint32_t sb = sc[j / 4 * 512 + j % 4];
-    const float s = FMT == GM_MX4 ? e8m0_value(sb) : e4m3_value(sb);
-    float v[8];
+    return FMT == GM_MX4 ? e8m0_value(sb) : e4m3_value(sb);
+  };
+  auto value = [&](uint32_t code, float f) {
+    const float v = __fmul_rn(e2m1_value(code), f);
+    return FMT == GM_NV4 ? __fmul_rn(v, gs) : v;
+  };
+  if (vec) {
+    // neighbouring lanes write neighbouring groups of four (n is a multiple of 4)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      v[e] = __fmul_rn(e2m1_value((w >> (4 * e)) & 15u), s);
-      if constexpr (FMT == GM_NV4) v[e] = __fmul_rn(v[e], gs);
+    for (int u = 0; u < kRowSpan / 128; ++u) {
+      const long long c = c0 + u * 128 + lane * 4;
+      if (c >= n) continue;
+      const uint32_t w = *reinterpret_cast<const uint16_t*>(row + c / 2);
+      const float f = factor(c);
+      store4_from_float(out, at + c, odt, make_float4(value(w & 15u, f), value(w >> 4 & 15u, f),
+                                                      value(w >> 8 & 15u, f), value(w >> 12, f)));
     }
-    const long long at = (b * (long long)m + r) * n + c;
-    if (vec && c + 8 <= n) {
-      store4_from_float(out, at, odt, make_float4(v[0], v[1], v[2], v[3]));
-      store4_from_float(out, at + 4, odt, make_float4(v[4], v[5], v[6], v[7]));
-    } else {
-      for (int e = 0; e < 8; ++e)
-        if (c + e < n) store_from_float(out, at + e, odt, v[e]);
+  } else {
+    // rows off alignment: neighbouring lanes write neighbouring elements
+#pragma unroll 8
+    for (int u = 0; u < kRowSpan / 32; ++u) {
+      const long long c = c0 + u * 32 + lane;
+      if (c >= n) break;
+      store_from_float(out, at + c, odt, value((uint32_t)row[c / 2] >> (4 * (c & 1)) & 15u, factor(c)));
     }
   }
 }
@@ -398,9 +424,9 @@ cudaError_t quant_t(int B, const QuantParams& p, cudaStream_t s) {
   if constexpr (FMT == GM_NV4) {
     cudaError_t e = cudaMemsetAsync(p.gscale, 0, (size_t)B * 4, s);
     if (e != cudaSuccess) return e;
-    const long long items = cdivll(p.n, 8) * p.m;
-    const long long want = cdivll(8LL * sm_count(), B);
-    const int gx = (int)(cdivll(items, kThreads) < want ? cdivll(items, kThreads) : want);
+    const long long blocks = cdivll(cdivll(p.n, kRowSpan) * p.m, kThreads / 32);
+    const long long want = cdivll(6LL * sm_count(), B);
+    const int gx = (int)(blocks < want ? blocks : want);
     k_mx4_top<DT><<<dim3(gx, B), kThreads, 0, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
