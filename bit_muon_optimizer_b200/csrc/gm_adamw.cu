@@ -132,12 +132,14 @@ __device__ __forceinline__ void e4m3x4_to_float(uint32_t w, float (&o)[4]) {
 __device__ __forceinline__ float root_value(uint32_t code) {
   return __fmul_rn(__uint_as_float(code << 19), 5.192296858534828e33f);   // 2^112
 }
-__device__ __forceinline__ uint32_t root_bits(float y) {
-  return __float_as_uint(__fmul_rn(y, 1.925929944387236e-34f));           // 2^-112
-}
-__device__ __forceinline__ float approx_sqrt(float x) {   // 2^-23
+__device__ __forceinline__ float approx_sqrt(float x) {   // 2^-22; x from 2^-126 on
   float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float approx_rcp(float x) {    // 2^-23
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -224,15 +226,16 @@ struct Codes8 {
   uint32_t m, v;
   float sm, sv;
 };
-struct Quad {
-  float x[4];
-};
-__device__ __noinline__ Codes8 exact_codes_of(const Consts& k, double c, Quad g, Quad mo, Quad ro, float ms, float vs) {
+__device__ __noinline__ Codes8 exact_codes(const Consts& k, double c, float g0, float g1, float g2, float g3,
+                                           uint32_t mc, uint32_t vc, float ms, float vs) {
+  const float g[4] = {g0, g1, g2, g3};
+  float mo[4];
+  e4m3x4_to_float(mc, mo);
   double dm[4], dv[4], xm = 0.0, xv = 0.0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const double gd = __dmul_rn((double)g.x[e], c);
-    const double rd = (double)ro.x[e] * (double)vs, md = (double)mo.x[e] * (double)ms;
+    const double gd = __dmul_rn((double)g[e], c);
+    const double rd = (double)root_value((vc >> (8 * e)) & 255u) * (double)vs, md = (double)mo[e] * (double)ms;
     dm[e] = __dadd_rn(__dmul_rn(k.db1, md), __dmul_rn(k.dob1, gd));
     dv[e] = __dadd_rn(__dmul_rn(k.db2, __dmul_rn(rd, rd)), __dmul_rn(k.dob2, __dmul_rn(gd, gd)));
     xm = fmax(xm, fabs(dm[e]));
@@ -248,140 +251,156 @@ __device__ __noinline__ Codes8 exact_codes_of(const Consts& k, double c, Quad g,
   }
   return o;
 }
-__device__ __forceinline__ Codes8 exact_codes(const Consts& k, double c, const float (&g)[4], const float (&mo)[4],
-                                              const float (&ro)[4], float ms, float vs) {
-  return exact_codes_of(k, c, Quad{g[0], g[1], g[2], g[3]}, Quad{mo[0], mo[1], mo[2], mo[3]},
-                        Quad{ro[0], ro[1], ro[2], ro[3]}, ms, vs);
+
+// Four elements a lane as they lie in memory.
+template <int PDT, int GDT, int BITS>
+struct Raw {
+  float p[4], g[4];
+  float m[4], v[4];        // 32-bit states
+  uint32_t mc, vc;         // 8-bit states
+  float ms, vs;
+};
+// FULL: the group lies inside the tensor and its arrays are aligned.
+template <int PDT, int GDT, int BITS, bool FULL>
+__device__ __forceinline__ void load_group(const Entry& E, long long i, int lane, bool aligned,
+                                           Raw<PDT, GDT, BITS>& x) {
+  const long long n = E.numel - i;
+  const bool vec = FULL || (aligned && n >= 4);
+  load4<PDT>(E.p, i, n, vec, x.p);
+  load4<GDT>(E.g, i, n, vec, x.g);
+  if constexpr (BITS == 32) {
+    load4<GM_F32>(E.m, i, n, vec, x.m);
+    load4<GM_F32>(E.v, i, n, vec, x.v);
+  } else {
+    x.mc = load4_codes(static_cast<const uint8_t*>(E.m), i, n, vec);
+    x.vc = load4_codes(static_cast<const uint8_t*>(E.v), i, n, vec);
+    const long long grp = i / kGroup8;
+    const bool in = FULL || n + lane * 4 > 0;
+    x.ms = in ? E.mscale[grp] : 0.f;
+    x.vs = in ? E.vscale[grp] : 0.f;
+  }
+}
+
+template <int PDT, int GDT, int BITS, bool FULL>
+__device__ __forceinline__ void step_group(const Entry& E, const Consts& k, const Coef* coef, const Coef& f,
+                                           long long i, int lane, bool aligned, Raw<PDT, GDT, BITS>& x) {
+  const long long n = E.numel - i;
+  const bool vec = FULL || (aligned && n >= 4);
+  if constexpr (BITS == 32) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float gc = x.g[e] * f.c32;
+      x.m[e] = fmaf(k.b1, x.m[e], k.ob1 * gc);
+      x.v[e] = fmaf(k.b2, x.v[e], gc * gc * k.ob2);
+      const float u = __fdiv_rn(x.m[e], fmaf(__fsqrt_rn(x.v[e]), f.root, k.eps));
+      x.p[e] = fmaf(x.p[e], f.decay, -u * f.scale);
+    }
+    store4(E.m, i, n, vec, GM_F32, x.m);
+    store4(E.v, i, n, vec, GM_F32, x.v);
+    store4(E.p, i, n, vec, PDT, x.p);
+    if (E.copy) store4(E.copy, i, n, vec, k.cdt, x.p);
+  } else {
+    float m[4], size[4], r[4];
+    uint32_t vb[4];
+    e4m3x4_to_float(x.mc, m);
+    uint32_t tmb = 0, tvb = 0;
+    float ts = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float gc = x.g[e] * f.c32;
+      const float r0 = root_value((x.vc >> (8 * e)) & 255u) * x.vs;
+      const float a = k.b1 * (m[e] * x.ms), b = k.ob1 * gc;
+      size[e] = fabsf(a) + fabsf(b);
+      m[e] = a + b;
+      const float v = fmaf(k.b2, r0 * r0, gc * gc * k.ob2);
+      // The approximations (2^-22 of an update) keep this kernel off its issue rate.
+      // v below 2^-126 has a root below 1.1e-19: zero beside any eps in use.
+      r[e] = approx_sqrt(fmaxf(v, kScaleFloor));
+      x.p[e] = fmaf(x.p[e], f.decay, -(m[e] * approx_rcp(fmaf(r[e], f.root, k.eps))) * f.scale);
+      // |x| as unsigned bits orders like the values; a NaN is above all of them
+      vb[e] = __float_as_uint(v) & 0x7FFFFFFFu;
+      tmb = max(tmb, __float_as_uint(fabsf(m[e])));
+      tvb = max(tvb, vb[e]);
+      ts = fmaxf(ts, size[e]);
+    }
+    store4(E.p, i, n, vec, PDT, x.p);
+    if (E.copy) store4(E.copy, i, n, vec, k.cdt, x.p);
+    const float tm = __uint_as_float(__reduce_max_sync(0xffffffffu, tmb));
+    const float tv = __uint_as_float(__reduce_max_sync(0xffffffffu, tvb));
+    float sm = scale_of(tm, 1.0f / kTopM), sv = scale_of(sqrtf(tv), 1.0f / kTopR);
+    // The stored codes are those of m and r in fp64 (each product and sum rounded
+    // singly, 1 / 448 and 1 / 1.9375 being constants: true ties occur, for m and r
+    // are made of short numbers, and the roundings decide them). fp32 decides a code
+    // unless its value lies so close to a border that its error could cross it;
+    // then the group is redone in fp64. Errors, u = 2^-24: m is off by 5 u size at
+    // most (two products of three roundings, one sum), and m / sm by that, by a few u,
+    // and by sm's relative error, 5 u size / tm of the top element: size up to 3 tm
+    // is allowed for, a group with more is redone. r is off by 12 u.
+    // Near fp32's subnormals these bounds do not hold: 2^-90 and 2^-80 keep the
+    // smallest element that gets a code (2^-18 of the top) and its square above them,
+    // and 2^14 keeps 1 / sv 2^112 below.
+    bool near = ts > 3.f * tm;
+    if (tm < 8.1e-28f || tv < 8.3e-25f || sv > 16384.f) near |= ts > 0.f || tvb > 0;
+    const float im = approx_rcp(sm), iv = approx_rcp(sv) * 1.925929944387236e-34f;   // 2^-112
+    const float w = im * 2.38418579e-6f;   // 5 * 2^-21: |m| <= size
+    float lo[4], hi[4];
+    uint32_t cv[4], gap = ~0u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float y = m[e] * im;
+      lo[e] = fmaf(size[e], -w, y);
+      hi[e] = fmaf(size[e], w, y);
+      // a border is at a set bit 18 with zeros below; +-32 around it
+      const uint32_t bits = __float_as_uint(r[e] * iv) + 0x40000u + 32u;
+      gap = min(gap, bits & 0x7FFFFu);
+      cv[e] = min(max(bits >> 19, 1u), vb[e]);   // 0 for v = 0 alone
+    }
+    uint32_t wm = e4m3x2(lo[0], lo[1]) | (e4m3x2(lo[2], lo[3]) << 16);
+    near |= gap <= 64u || wm != (e4m3x2(hi[0], hi[1]) | (e4m3x2(hi[2], hi[3]) << 16));
+    uint32_t wv = cv[0] | (cv[1] << 8) | (cv[2] << 16) | (cv[3] << 24);
+    if (__any_sync(0xffffffffu, near) && tm <= 3.402823466e38f && tv <= 3.402823466e38f) {
+      const Codes8 o = exact_codes(k, coef->c, x.g[0], x.g[1], x.g[2], x.g[3], x.mc, x.vc, x.ms, x.vs);
+      wm = o.m;
+      wv = o.v;
+      sm = o.sm;
+      sv = o.sv;
+    }
+    store4_codes(static_cast<uint8_t*>(E.m), i, n, vec, wm);
+    store4_codes(static_cast<uint8_t*>(E.v), i, n, vec, wv);
+    if (lane == 0) {
+      E.mscale[i / kGroup8] = sm;
+      E.vscale[i / kGroup8] = sv;
+    }
+  }
 }
 
 template <int PDT, int GDT, int BITS>
-__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Table t, const Consts k,
-                                                    const Coef* __restrict__ coef) {
+__global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ Table t, const Consts k,
+                                                       const Coef* __restrict__ coef) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (coef->skip) return;
-  const float c = coef->c32, decay = coef->decay, scale = coef->scale, root = coef->root;
+  const Coef f = *coef;
+  if (f.skip) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int ti = 0;
   for (int chunk = blockIdx.x; chunk < t.map.total(); chunk += gridDim.x) {
     ti = t.map.find(chunk, ti);
     const Entry& E = t.e[ti];
     const long long base = (long long)(chunk - t.map.first[ti]) * kChunk + warp * (kUnroll * kGroup8);
-    const long long left = E.numel - base;   // of this warp's part
-    if (left <= 0) continue;
-    float p[kUnroll][4], g[kUnroll][4], m[kUnroll][4], v[kUnroll][4];
-    uint32_t mc[kUnroll], vc[kUnroll];
-    float ms[kUnroll], vs[kUnroll];
     const bool aligned = t.vec[ti] != 0;
+    Raw<PDT, GDT, BITS> x[kUnroll];
+    if (aligned && base + kUnroll * kGroup8 <= E.numel) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const long long i = base + u * kGroup8 + lane * 4, n = E.numel - i;
-      const bool vec = aligned && n >= 4;
-      load4<PDT>(E.p, i, n, vec, p[u]);
-      load4<GDT>(E.g, i, n, vec, g[u]);
-      if constexpr (BITS == 32) {
-        load4<GM_F32>(E.m, i, n, vec, m[u]);
-        load4<GM_F32>(E.v, i, n, vec, v[u]);
-      } else {
-        mc[u] = load4_codes(static_cast<const uint8_t*>(E.m), i, n, vec);
-        vc[u] = load4_codes(static_cast<const uint8_t*>(E.v), i, n, vec);
-        const bool in = left > u * kGroup8;
-        const long long grp = base / kGroup8 + u;
-        ms[u] = in ? E.mscale[grp] : 0.f;
-        vs[u] = in ? E.vscale[grp] : 0.f;
-      }
-    }
+      for (int u = 0; u < kUnroll; ++u)
+        load_group<PDT, GDT, BITS, true>(E, base + u * kGroup8 + lane * 4, lane, true, x[u]);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const long long i = base + u * kGroup8 + lane * 4, n = E.numel - i;
-      const bool vec = aligned && n >= 4;
-      float mo[4], ro[4];          // decoded m and r (8-bit states)
-      if constexpr (BITS == 8) {
-        e4m3x4_to_float(mc[u], mo);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          m[u][e] = __fmul_rn(mo[e], ms[u]);
-          ro[e] = root_value((vc[u] >> (8 * e)) & 255u);
-          const float r = __fmul_rn(ro[e], vs[u]);
-          v[u][e] = __fmul_rn(r, r);
-        }
-      }
-      float size[4], r[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float gc = g[u][e] * c;
-        const float a = k.b1 * m[u][e], b = k.ob1 * gc;
-        size[e] = fabsf(a) + fabsf(b);
-        m[u][e] = a + b;
-        v[u][e] = fmaf(k.b2, v[u][e], gc * gc * k.ob2);
-        if constexpr (BITS == 32) {
-          r[e] = __fsqrt_rn(v[u][e]);
-          p[u][e] = fmaf(p[u][e], decay, -__fdiv_rn(m[u][e], fmaf(r[e], root, k.eps)) * scale);
-        } else {
-          // 2^-22 of an update: IEEE roots and quotients would bound this kernel by its issue rate
-          r[e] = approx_sqrt(v[u][e]);
-          p[u][e] = fmaf(p[u][e], decay, -__fdividef(m[u][e], fmaf(r[e], root, k.eps)) * scale);
-        }
-      }
-      store4(E.p, i, n, vec, PDT, p[u]);
-      if (E.copy) store4(E.copy, i, n, vec, k.cdt, p[u]);
-      if constexpr (BITS == 32) {
-        store4(E.m, i, n, vec, GM_F32, m[u]);
-        store4(E.v, i, n, vec, GM_F32, v[u]);
-      } else {
-        if (left <= u * kGroup8) continue;   // the whole warp
-        // |x| as unsigned bits orders like the values; a NaN is above all of them
-        uint32_t am = 0, ar = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          am = max(am, __float_as_uint(fabsf(m[u][e])));
-          ar = max(ar, __float_as_uint(fabsf(r[e])));
-        }
-        const float tm = __uint_as_float(__reduce_max_sync(0xffffffffu, am));
-        const float tr = __uint_as_float(__reduce_max_sync(0xffffffffu, ar));
-        float sm = scale_of(tm, 1.0f / kTopM), sv = scale_of(tr, 1.0f / kTopR);
-        const float im = __frcp_rn(sm), iv = __frcp_rn(sv);
-        // The stored codes are those of m and r in fp64 (each product and sum rounded
-        // singly, 1 / 448 and 1 / 1.9375 being constants: true ties occur, for m and r
-        // are made of short numbers, and the roundings decide them). fp32 decides a code
-        // unless its value lies so close to a border that its error could cross it;
-        // then the group is redone in fp64. Errors, u = 2^-24: m is off by 5 u size
-        // at most (two products of three roundings, one sum), and m / sm by that and by
-        // sm's relative error, 5 u size / tm of the top element plus a few u: size up
-        // to 3 tm is allowed for, a group with more is redone. r is off by 10 u.
-        // Near fp32's subnormals these bounds do not hold: 2^-90 and 2^-40 keep the
-        // smallest element that gets a code (2^-18 of the top) and its square above them.
-        bool near = (tm > 0.f && tm < 8.1e-28f) || (tr > 0.f && tr < 9.1e-13f);
-        const float wide = 3.f * tm, w21 = im * 4.76837158e-7f;   // 2^-21
-        float lo[4], hi[4];
-        uint32_t cv[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          near |= size[e] > wide;
-          const float d = fmaf(fabsf(m[u][e]), 4.f, size[e]) * w21;
-          lo[e] = fmaf(m[u][e], im, -d);
-          hi[e] = fmaf(m[u][e], im, d);
-          // the code's border is at a set bit 18 with zeros below; +-32 around it
-          const uint32_t bits = root_bits(r[e] * iv) + 0x40000u + 32u;
-          near |= (bits & 0x7FFFFu) <= 64u;
-          cv[e] = max(bits >> 19, min(__float_as_uint(v[u][e]), 1u));
-        }
-        uint32_t wm = e4m3x2(lo[0], lo[1]) | (e4m3x2(lo[2], lo[3]) << 16);
-        near |= wm != (e4m3x2(hi[0], hi[1]) | (e4m3x2(hi[2], hi[3]) << 16));
-        uint32_t wv = cv[0] | (cv[1] << 8) | (cv[2] << 16) | (cv[3] << 24);
-        if (__any_sync(0xffffffffu, near) && tm <= 3.402823466e38f && tr <= 3.402823466e38f) {
-          const Codes8 x = exact_codes(k, coef->c, g[u], mo, ro, ms[u], vs[u]);
-          wm = x.m;
-          wv = x.v;
-          sm = x.sm;
-          sv = x.sv;
-        }
-        store4_codes(static_cast<uint8_t*>(E.m), i, n, vec, wm);
-        store4_codes(static_cast<uint8_t*>(E.v), i, n, vec, wv);
-        if (lane == 0) {
-          const long long grp = base / kGroup8 + u;
-          E.mscale[grp] = sm;
-          E.vscale[grp] = sv;
-        }
+      for (int u = 0; u < kUnroll; ++u)
+        step_group<PDT, GDT, BITS, true>(E, k, coef, f, base + u * kGroup8 + lane * 4, lane, true, x[u]);
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < kUnroll && base + u * kGroup8 < E.numel; ++u) {
+        const long long i = base + u * kGroup8 + lane * 4;
+        load_group<PDT, GDT, BITS, false>(E, i, lane, aligned, x[0]);
+        step_group<PDT, GDT, BITS, false>(E, k, coef, f, i, lane, aligned, x[0]);
       }
     }
   }
@@ -604,7 +623,7 @@ cudaError_t launch_adamw(int count, const gm_adamw_tensor* tensors, int pdt, int
                  aligned_to(x.copy, 4 * width(cdt));
     }
     const int total = t.map.first[n];
-    const int grid = total < 8 * sm_count() ? total : 8 * sm_count();
+    const int grid = total < 4 * sm_count() ? total : 4 * sm_count();   // all resident
     e = launch_after(kernel, grid, s, t, k, static_cast<const Coef*>(scratch));
     if (e != cudaSuccess) return e;
   }
