@@ -45,56 +45,68 @@ struct ChunkMap {
 };
 
 // ------------------------------------------------------------------ load / store
-// Four consecutive elements from i on, `n` of them inside the tensor (n <= 0:
-// none). `vec`: the array is aligned for one vector access and n >= 4.
+// Eight consecutive elements from i on, `n` of them inside the tensor (n <= 0:
+// none). WHOLE: all of them, and the array is aligned to eight elements.
 template <int DT>
 __device__ __forceinline__ float one(const void* p, long long i) {
   if constexpr (DT == GM_F32) return static_cast<const float*>(p)[i];
   else return h16_to_float(static_cast<const uint16_t*>(p)[i], DT == GM_F16);
 }
-template <int DT>
-__device__ __forceinline__ void load4(const void* p, long long i, long long n, bool vec, float (&o)[4]) {
-  if (vec) {
-    if constexpr (DT == GM_F32) {
-      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-      o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
-    } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-      o[0] = h16_to_float((uint16_t)(v.x & 0xFFFFu), DT == GM_F16);
-      o[1] = h16_to_float((uint16_t)(v.x >> 16), DT == GM_F16);
-      o[2] = h16_to_float((uint16_t)(v.y & 0xFFFFu), DT == GM_F16);
-      o[3] = h16_to_float((uint16_t)(v.y >> 16), DT == GM_F16);
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void load8(const void* p, long long i, long long n, float (&o)[8]) {
+  if constexpr (!WHOLE) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = e < n ? one<DT>(p, i + e) : 0.f;
+  } else if constexpr (DT == GM_F32) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
+                 : "l"(static_cast<const float*>(p) + i)
+                 : "memory");
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      o[2 * j] = h16_to_float((uint16_t)(w[j] & 0xFFFFu), DT == GM_F16);
+      o[2 * j + 1] = h16_to_float((uint16_t)(w[j] >> 16), DT == GM_F16);
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = e < n ? one<DT>(p, i + e) : 0.f;
   }
 }
-__device__ __forceinline__ void store4(void* p, long long i, long long n, bool vec, int dt,
-                                       const float (&v)[4]) {
-  if (vec) {
-    store4_from_float(p, i, dt, make_float4(v[0], v[1], v[2], v[3]));
-  } else {
+template <bool WHOLE>
+__device__ __forceinline__ void store8(void* p, long long i, long long n, int dt, const float (&v)[8]) {
+  if constexpr (!WHOLE) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < 8; ++e)
       if (e < n) store_from_float(p, i + e, dt, v[e]);
+  } else if (dt == GM_F32) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<float*>(p) + i),
+                 "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = (uint32_t)float_to_h16(v[2 * j], dt == GM_F16) | ((uint32_t)float_to_h16(v[2 * j + 1], dt == GM_F16) << 16);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-__device__ __forceinline__ uint32_t load4_codes(const uint8_t* p, long long i, long long n, bool vec) {
-  if (vec) return *reinterpret_cast<const uint32_t*>(p + i);
-  uint32_t w = 0;
+template <bool WHOLE>
+__device__ __forceinline__ uint2 load8_codes(const uint8_t* p, long long i, long long n) {
+  if constexpr (WHOLE) return *reinterpret_cast<const uint2*>(p + i);
+  uint32_t w[2] = {0, 0};
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < n) w |= (uint32_t)p[i + e] << (8 * e);
-  return w;
+  for (int e = 0; e < 8; ++e)
+    if (e < n) w[e >> 2] |= (uint32_t)p[i + e] << (8 * (e & 3));
+  return make_uint2(w[0], w[1]);
 }
-__device__ __forceinline__ void store4_codes(uint8_t* p, long long i, long long n, bool vec, uint32_t w) {
-  if (vec) {
-    *reinterpret_cast<uint32_t*>(p + i) = w;
+template <bool WHOLE>
+__device__ __forceinline__ void store8_codes(uint8_t* p, long long i, long long n, uint2 w) {
+  if constexpr (WHOLE) {
+    *reinterpret_cast<uint2*>(p + i) = w;
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < n) p[i + e] = (uint8_t)(w >> (8 * e));
+    for (int e = 0; e < 8; ++e)
+      if (e < n) p[i + e] = (uint8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3)));
   }
 }
 
@@ -143,6 +155,12 @@ __device__ __forceinline__ float approx_rcp(float x) {    // 2^-23
   return r;
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {   // a NaN where either is one
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Both codes from fp64 values (round to nearest, ties to even).
 __device__ __forceinline__ double pow2d(int e) { return __hiloint2double((e + 1023) << 20, 0); }
 __device__ __forceinline__ uint32_t e4m3_from_double(double y) {
@@ -158,9 +176,15 @@ __device__ __forceinline__ uint32_t root_from_double(double y, double v) {
   return (float)v > 0.f ? max(c, 1u) : c;
 }
 
-__device__ __forceinline__ double warp_max(double x) {
+// Maxima over the 16 lanes that hold a group.
+__device__ __forceinline__ double group_max(double x) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) x = fmax(x, __shfl_xor_sync(0xffffffffu, x, o));
+  for (int o = 8; o; o >>= 1) x = fmax(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ uint32_t group_max(uint32_t x) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
 }
 
@@ -172,12 +196,13 @@ struct Coef {
   float decay;       // 1 - lr wd
   float scale;       // lr / (1 - b1^t)
   float root;        // 1 / sqrt(1 - b2^t)
+  float root8, eps8; // root / scale, eps / scale: the update is m / (r root8 + eps8)
   int skip;
 };
 static_assert(sizeof(Coef) <= GM_ADAMW_SCRATCH_BYTES, "the step's scratch holds the coefficients");
 
-__global__ void k_adamw_begin(double lr, double b1, double b2, double wd, const double* clip,
-                              const float* lr_dev, const int32_t* skip, int64_t* step, Coef* out) {
+__global__ void k_adamw_begin(double lr, double b1, double b2, double eps, double wd,
+                              const double* clip, const float* lr_dev, const int32_t* skip, int64_t* step, Coef* out) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (skip && *skip) {
     out->skip = 1;
@@ -190,8 +215,12 @@ __global__ void k_adamw_begin(double lr, double b1, double b2, double wd, const 
   out->c = c;
   out->c32 = (float)c;
   out->decay = (float)(1.0 - l * wd);
-  out->scale = (float)(l / (1.0 - pow(b1, (double)t)));
-  out->root = (float)(1.0 / sqrt(1.0 - pow(b2, (double)t)));
+  const double s = l / (1.0 - pow(b1, (double)t)), r = 1.0 / sqrt(1.0 - pow(b2, (double)t));
+  out->scale = (float)s;
+  out->root = (float)r;
+  // a rate of zero: a denominator whose reciprocal is zero
+  out->root8 = fabs(s) > 1e-20 ? (float)(r / s) : 0.f;
+  out->eps8 = fabs(s) > 1e-20 ? (float)(eps / s) : 3e38f;
   out->skip = 0;
 }
 
@@ -213,169 +242,181 @@ struct Table {
 };
 struct Consts {
   float b1, ob1, b2, ob2, eps;   // ob = 1 - b, rounded once from fp64
+  float rb2, rob2;               // roots of b2 and ob2
   double db1, dob1, db2, dob2;
   int cdt;
 };
 
-constexpr int kUnroll = 2;                                    // groups of a warp in flight
-constexpr int kChunk = kWarps * kUnroll * kGroup8;
+constexpr int kPart = 256;                  // elements of a warp at a time: two groups, eight a lane
+constexpr int kChunk = kWarps * kPart;
 
-// The codes and scales of a group in fp64, four elements a lane (kept out of line:
-// one group in a few hundred comes here).
+// The codes and scales of two groups in fp64, eight elements a lane (kept out of
+// line: one part in thirty comes here).
 struct Codes8 {
-  uint32_t m, v;
+  uint2 m, v;
   float sm, sv;
 };
-__device__ __noinline__ Codes8 exact_codes(const Consts& k, double c, float g0, float g1, float g2, float g3,
-                                           uint32_t mc, uint32_t vc, float ms, float vs) {
-  const float g[4] = {g0, g1, g2, g3};
-  float mo[4];
-  e4m3x4_to_float(mc, mo);
-  double dm[4], dv[4], xm = 0.0, xv = 0.0;
+struct Eight {
+  float x[8];
+};
+__device__ __noinline__ Codes8 exact_codes(const Consts& k, double c, Eight g, uint2 mc, uint2 vc, float ms, float vs) {
+  float mo[8], ml[4], mh[4];
+  e4m3x4_to_float(mc.x, ml);
+  e4m3x4_to_float(mc.y, mh);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const double gd = __dmul_rn((double)g[e], c);
-    const double rd = (double)root_value((vc >> (8 * e)) & 255u) * (double)vs, md = (double)mo[e] * (double)ms;
+  for (int e = 0; e < 8; ++e) mo[e] = e < 4 ? ml[e & 3] : mh[e & 3];
+  double dm[8], dv[8], xm = 0.0, xv = 0.0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const double gd = __dmul_rn((double)g.x[e], c);
+    const double rd = (double)root_value((e < 4 ? vc.x : vc.y) >> (8 * (e & 3)) & 255u) * (double)vs;
+    const double md = (double)mo[e] * (double)ms;
     dm[e] = __dadd_rn(__dmul_rn(k.db1, md), __dmul_rn(k.dob1, gd));
     dv[e] = __dadd_rn(__dmul_rn(k.db2, __dmul_rn(rd, rd)), __dmul_rn(k.dob2, __dmul_rn(gd, gd)));
     xm = fmax(xm, fabs(dm[e]));
     xv = fmax(xv, dv[e]);
   }
-  const double dsm = fmax(__dmul_rn(warp_max(xm), 1.0 / 448.0), pow2d(-126));
-  const double dsv = fmax(__dmul_rn(sqrt(warp_max(xv)), 1.0 / 1.9375), pow2d(-126));
-  Codes8 o{0, 0, (float)dsm, (float)dsv};
+  const double dsm = fmax(__dmul_rn(group_max(xm), 1.0 / 448.0), pow2d(-126));
+  const double dsv = fmax(__dmul_rn(sqrt(group_max(xv)), 1.0 / 1.9375), pow2d(-126));
+  Codes8 o{make_uint2(0, 0), make_uint2(0, 0), (float)dsm, (float)dsv};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    o.m |= e4m3_from_double(dm[e] / dsm) << (8 * e);
-    o.v |= root_from_double(sqrt(dv[e]) / dsv, dv[e]) << (8 * e);
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t a = e4m3_from_double(dm[e] / dsm) << (8 * (e & 3));
+    const uint32_t b = root_from_double(sqrt(dv[e]) / dsv, dv[e]) << (8 * (e & 3));
+    if (e < 4) {
+      o.m.x |= a;
+      o.v.x |= b;
+    } else {
+      o.m.y |= a;
+      o.v.y |= b;
+    }
   }
   return o;
 }
 
-// Four elements a lane as they lie in memory.
-template <int PDT, int GDT, int BITS>
-struct Raw {
-  float p[4], g[4];
-  float m[4], v[4];        // 32-bit states
-  uint32_t mc, vc;         // 8-bit states
-  float ms, vs;
-};
-// FULL: the group lies inside the tensor and its arrays are aligned.
-template <int PDT, int GDT, int BITS, bool FULL>
-__device__ __forceinline__ void load_group(const Entry& E, long long i, int lane, bool aligned,
-                                           Raw<PDT, GDT, BITS>& x) {
-  const long long n = E.numel - i;
-  const bool vec = FULL || (aligned && n >= 4);
-  load4<PDT>(E.p, i, n, vec, x.p);
-  load4<GDT>(E.g, i, n, vec, x.g);
-  if constexpr (BITS == 32) {
-    load4<GM_F32>(E.m, i, n, vec, x.m);
-    load4<GM_F32>(E.v, i, n, vec, x.v);
-  } else {
-    x.mc = load4_codes(static_cast<const uint8_t*>(E.m), i, n, vec);
-    x.vc = load4_codes(static_cast<const uint8_t*>(E.v), i, n, vec);
-    const long long grp = i / kGroup8;
-    const bool in = FULL || n + lane * 4 > 0;
-    x.ms = in ? E.mscale[grp] : 0.f;
-    x.vs = in ? E.vscale[grp] : 0.f;
-  }
+__device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-template <int PDT, int GDT, int BITS, bool FULL>
-__device__ __forceinline__ void step_group(const Entry& E, const Consts& k, const Coef* coef, const Coef& f,
-                                           long long i, int lane, bool aligned, Raw<PDT, GDT, BITS>& x) {
+// Eight elements a lane, element i the first. WHOLE: the warp's part lies inside the
+// tensor, whose arrays are aligned to eight elements.
+template <int PDT, int GDT, int BITS, bool WHOLE>
+__device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const Coef* coef, const Coef& f,
+                                          long long i, int lane) {
   const long long n = E.numel - i;
-  const bool vec = FULL || (aligned && n >= 4);
+  float p[8], g[8];
+  load8<PDT, WHOLE>(E.p, i, n, p);
+  load8<GDT, WHOLE>(E.g, i, n, g);
   if constexpr (BITS == 32) {
+    float m[8], v[8];
+    load8<GM_F32, WHOLE>(E.m, i, n, m);
+    load8<GM_F32, WHOLE>(E.v, i, n, v);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float gc = x.g[e] * f.c32;
-      x.m[e] = fmaf(k.b1, x.m[e], k.ob1 * gc);
-      x.v[e] = fmaf(k.b2, x.v[e], gc * gc * k.ob2);
-      const float u = __fdiv_rn(x.m[e], fmaf(__fsqrt_rn(x.v[e]), f.root, k.eps));
-      x.p[e] = fmaf(x.p[e], f.decay, -u * f.scale);
+    for (int e = 0; e < 8; ++e) {
+      const float gc = g[e] * f.c32;
+      m[e] = fmaf(k.b1, m[e], k.ob1 * gc);
+      v[e] = fmaf(k.b2, v[e], gc * gc * k.ob2);
+      const float u = __fdiv_rn(m[e], fmaf(__fsqrt_rn(v[e]), f.root, k.eps));
+      p[e] = fmaf(p[e], f.decay, -u * f.scale);
     }
-    store4(E.m, i, n, vec, GM_F32, x.m);
-    store4(E.v, i, n, vec, GM_F32, x.v);
-    store4(E.p, i, n, vec, PDT, x.p);
-    if (E.copy) store4(E.copy, i, n, vec, k.cdt, x.p);
+    store8<WHOLE>(E.m, i, n, GM_F32, m);
+    store8<WHOLE>(E.v, i, n, GM_F32, v);
+    store8<WHOLE>(E.p, i, n, PDT, p);
+    if (E.copy) store8<WHOLE>(E.copy, i, n, k.cdt, p);
   } else {
-    float m[4], size[4], r[4];
-    uint32_t vb[4];
-    e4m3x4_to_float(x.mc, m);
-    uint32_t tmb = 0, tvb = 0;
-    float ts = 0.f;
+    const long long grp = i / kGroup8;
+    const bool in = WHOLE || n + (lane & 15) * 8 > 0;     // the group begins inside the tensor
+    const uint2 mc = load8_codes<WHOLE>(static_cast<const uint8_t*>(E.m), i, n);
+    const uint2 vc = load8_codes<WHOLE>(static_cast<const uint8_t*>(E.v), i, n);
+    const float ms = in ? E.mscale[grp] : 0.f, vs = in ? E.vscale[grp] : 0.f;
+    // b1 sm and the roots of b2 and 1 - b2 go into the group's factors:
+    // m' = code (b1 sm) + g (1 - b1) c, v' = (root sv sqrt(b2))^2 + (g c sqrt(1 - b2))^2
+    const float ma = k.b1 * ms, va = k.rb2 * vs, cm = k.ob1 * f.c32, cv = k.rob2 * f.c32;
+    float m[8], size[8], r[8];
+    uint32_t vb[8];
+    {
+      float ml[4], mh[4];
+      e4m3x4_to_float(mc.x, ml);
+      e4m3x4_to_float(mc.y, mh);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float gc = x.g[e] * f.c32;
-      const float r0 = root_value((x.vc >> (8 * e)) & 255u) * x.vs;
-      const float a = k.b1 * (m[e] * x.ms), b = k.ob1 * gc;
+      for (int e = 0; e < 8; ++e) m[e] = e < 4 ? ml[e & 3] : mh[e & 3];
+    }
+    float tm = 0.f, ts = 0.f;
+    uint32_t tvb = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float a = m[e] * ma, b = g[e] * cm;
+      const float r0 = root_value((e < 4 ? vc.x : vc.y) >> (8 * (e & 3)) & 255u) * va, g0 = g[e] * cv;
       size[e] = fabsf(a) + fabsf(b);
       m[e] = a + b;
-      const float v = fmaf(k.b2, r0 * r0, gc * gc * k.ob2);
-      // The approximations (2^-22 of an update) keep this kernel off its issue rate.
-      // v below 2^-126 has a root below 1.1e-19: zero beside any eps in use.
-      r[e] = approx_sqrt(fmaxf(v, kScaleFloor));
-      x.p[e] = fmaf(x.p[e], f.decay, -(m[e] * approx_rcp(fmaf(r[e], f.root, k.eps))) * f.scale);
-      // |x| as unsigned bits orders like the values; a NaN is above all of them
-      vb[e] = __float_as_uint(v) & 0x7FFFFFFFu;
-      tmb = max(tmb, __float_as_uint(fabsf(m[e])));
+      const float v = fmaf(r0, r0, g0 * g0);
+      // Approximations (2^-21 of an update) and factors taken out of the loop keep this
+      // kernel off its issue rate. A v below 2^-126 has a root below 1.1e-19, taken as
+      // zero: nothing beside an eps of 1e-15.
+      r[e] = approx_sqrt(v);
+      p[e] = fmaf(p[e], f.decay, -m[e] * approx_rcp(fmaf(r[e], f.root8, f.eps8)));
+      vb[e] = __float_as_uint(v);     // never negative: ordered like the values, a NaN above
+      tm = max_nan(tm, fabsf(m[e]));
       tvb = max(tvb, vb[e]);
       ts = fmaxf(ts, size[e]);
     }
-    store4(E.p, i, n, vec, PDT, x.p);
-    if (E.copy) store4(E.copy, i, n, vec, k.cdt, x.p);
-    const float tm = __uint_as_float(__reduce_max_sync(0xffffffffu, tmb));
-    const float tv = __uint_as_float(__reduce_max_sync(0xffffffffu, tvb));
-    float sm = scale_of(tm, 1.0f / kTopM), sv = scale_of(sqrtf(tv), 1.0f / kTopR);
+    store8<WHOLE>(E.p, i, n, PDT, p);
+    if (E.copy) store8<WHOLE>(E.copy, i, n, k.cdt, p);
+    tm = __uint_as_float(group_max(__float_as_uint(tm)));
+    const float tv = __uint_as_float(group_max(tvb));
+    float sm = scale_of(tm, 1.0f / kTopM), sv = scale_of(approx_sqrt(tv), 1.0f / kTopR);
     // The stored codes are those of m and r in fp64 (each product and sum rounded
     // singly, 1 / 448 and 1 / 1.9375 being constants: true ties occur, for m and r
     // are made of short numbers, and the roundings decide them). fp32 decides a code
     // unless its value lies so close to a border that its error could cross it;
-    // then the group is redone in fp64. Errors, u = 2^-24: m is off by 5 u size at
-    // most (two products of three roundings, one sum), and m / sm by that, by a few u,
-    // and by sm's relative error, 5 u size / tm of the top element: size up to 3 tm
-    // is allowed for, a group with more is redone. r is off by 12 u.
+    // then the groups are redone in fp64. Errors, u = 2^-24: m is off by 5 u size at
+    // most (two products of three roundings, one sum), and m / sm by that, by 6 u, and
+    // by sm's relative error, 5 u size / tm of the top element: size up to 3 tm is
+    // allowed for (26 u size in all), a group with more is redone. r is off by 16 u.
     // Near fp32's subnormals these bounds do not hold: 2^-90 and 2^-80 keep the
     // smallest element that gets a code (2^-18 of the top) and its square above them,
     // and 2^14 keeps 1 / sv 2^112 below.
     bool near = ts > 3.f * tm;
     if (tm < 8.1e-28f || tv < 8.3e-25f || sv > 16384.f) near |= ts > 0.f || tvb > 0;
     const float im = approx_rcp(sm), iv = approx_rcp(sv) * 1.925929944387236e-34f;   // 2^-112
-    const float w = im * 2.38418579e-6f;   // 5 * 2^-21: |m| <= size
-    float lo[4], hi[4];
-    uint32_t cv[4], gap = ~0u;
+    const float w = im * 1.66893005e-6f;   // 28 u
+    float lo[8], hi[8];
+    uint32_t cr[8], gap = ~0u;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 8; ++e) {
       const float y = m[e] * im;
       lo[e] = fmaf(size[e], -w, y);
       hi[e] = fmaf(size[e], w, y);
-      // a border is at a set bit 18 with zeros below; +-32 around it
-      const uint32_t bits = __float_as_uint(r[e] * iv) + 0x40000u + 32u;
+      // a border is at a set bit 18 with zeros below; +-20 around it
+      const uint32_t bits = __float_as_uint(r[e] * iv) + 0x40000u + 20u;
       gap = min(gap, bits & 0x7FFFFu);
-      cv[e] = min(max(bits >> 19, 1u), vb[e]);   // 0 for v = 0 alone
+      cr[e] = max(bits >> 19, min(vb[e], 1u));
     }
-    uint32_t wm = e4m3x2(lo[0], lo[1]) | (e4m3x2(lo[2], lo[3]) << 16);
-    near |= gap <= 64u || wm != (e4m3x2(hi[0], hi[1]) | (e4m3x2(hi[2], hi[3]) << 16));
-    uint32_t wv = cv[0] | (cv[1] << 8) | (cv[2] << 16) | (cv[3] << 24);
-    if (__any_sync(0xffffffffu, near) && tm <= 3.402823466e38f && tv <= 3.402823466e38f) {
-      const Codes8 o = exact_codes(k, coef->c, x.g[0], x.g[1], x.g[2], x.g[3], x.mc, x.vc, x.ms, x.vs);
-      wm = o.m;
-      wv = o.v;
-      sm = o.sm;
-      sv = o.sv;
+    uint2 wm = make_uint2(e4m3x2(lo[0], lo[1]) | (e4m3x2(lo[2], lo[3]) << 16),
+                          e4m3x2(lo[4], lo[5]) | (e4m3x2(lo[6], lo[7]) << 16));
+    near |= gap <= 40u || wm.x != (e4m3x2(hi[0], hi[1]) | (e4m3x2(hi[2], hi[3]) << 16)) ||
+            wm.y != (e4m3x2(hi[4], hi[5]) | (e4m3x2(hi[6], hi[7]) << 16));
+    uint2 wv = make_uint2(bytes4(cr[0], cr[1], cr[2], cr[3]), bytes4(cr[4], cr[5], cr[6], cr[7]));
+    if (__any_sync(0xffffffffu, near)) {
+      const Codes8 o = exact_codes(k, coef->c, Eight{g[0], g[1], g[2], g[3], g[4], g[5], g[6], g[7]}, mc, vc, ms, vs);
+      if (tm <= 3.402823466e38f && tv <= 3.402823466e38f) {   // else the group is NaN
+        wm = o.m;
+        wv = o.v;
+        sm = o.sm;
+        sv = o.sv;
+      }
     }
-    store4_codes(static_cast<uint8_t*>(E.m), i, n, vec, wm);
-    store4_codes(static_cast<uint8_t*>(E.v), i, n, vec, wv);
-    if (lane == 0) {
-      E.mscale[i / kGroup8] = sm;
-      E.vscale[i / kGroup8] = sv;
+    store8_codes<WHOLE>(static_cast<uint8_t*>(E.m), i, n, wm);
+    store8_codes<WHOLE>(static_cast<uint8_t*>(E.v), i, n, wv);
+    if ((lane & 15) == 0 && in) {
+      E.mscale[grp] = sm;
+      E.vscale[grp] = sv;
     }
   }
 }
 
 template <int PDT, int GDT, int BITS>
-__global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ Table t, const Consts k,
+__global__ void __launch_bounds__(kThreads, 3) k_adamw(const __grid_constant__ Table t, const Consts k,
                                                        const Coef* __restrict__ coef) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Coef f = *coef;
@@ -385,24 +426,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_adamw(const __grid_constant__ T
   for (int chunk = blockIdx.x; chunk < t.map.total(); chunk += gridDim.x) {
     ti = t.map.find(chunk, ti);
     const Entry& E = t.e[ti];
-    const long long base = (long long)(chunk - t.map.first[ti]) * kChunk + warp * (kUnroll * kGroup8);
-    const bool aligned = t.vec[ti] != 0;
-    Raw<PDT, GDT, BITS> x[kUnroll];
-    if (aligned && base + kUnroll * kGroup8 <= E.numel) {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-        load_group<PDT, GDT, BITS, true>(E, base + u * kGroup8 + lane * 4, lane, true, x[u]);
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-        step_group<PDT, GDT, BITS, true>(E, k, coef, f, base + u * kGroup8 + lane * 4, lane, true, x[u]);
-    } else {
-#pragma unroll 1
-      for (int u = 0; u < kUnroll && base + u * kGroup8 < E.numel; ++u) {
-        const long long i = base + u * kGroup8 + lane * 4;
-        load_group<PDT, GDT, BITS, false>(E, i, lane, aligned, x[0]);
-        step_group<PDT, GDT, BITS, false>(E, k, coef, f, i, lane, aligned, x[0]);
-      }
-    }
+    const long long base = (long long)(chunk - t.map.first[ti]) * kChunk + warp * kPart;
+    if (t.vec[ti] && base + kPart <= E.numel)
+      step_part<PDT, GDT, BITS, true>(E, k, coef, f, base + lane * 8, lane);
+    else if (base < E.numel)
+      step_part<PDT, GDT, BITS, false>(E, k, coef, f, base + lane * 8, lane);
   }
 }
 
@@ -423,31 +451,33 @@ struct UnpackTable {
   UnpackEntry e[kMaxUnpack];
 };
 
+template <bool WHOLE>
+__device__ __forceinline__ void unpack_part(const UnpackEntry& E, long long i) {
+  const long long n = E.numel - i;
+  const uint2 mc = load8_codes<WHOLE>(E.m, i, n), vc = load8_codes<WHOLE>(E.v, i, n);
+  const float ms = E.mscale[i / kGroup8], vs = E.vscale[i / kGroup8];
+  float ml[4], mh[4], m[8], v[8];
+  e4m3x4_to_float(mc.x, ml);
+  e4m3x4_to_float(mc.y, mh);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    m[e] = __fmul_rn(e < 4 ? ml[e & 3] : mh[e & 3], ms);
+    const float r = __fmul_rn(root_value((e < 4 ? vc.x : vc.y) >> (8 * (e & 3)) & 255u), vs);
+    v[e] = __fmul_rn(r, r);
+  }
+  store8<WHOLE>(E.m_out, i, n, GM_F32, m);
+  store8<WHOLE>(E.v_out, i, n, GM_F32, v);
+}
+
 __global__ void __launch_bounds__(kThreads) k_adamw_unpack8(const __grid_constant__ UnpackTable t) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int ti = 0;
   for (int chunk = blockIdx.x; chunk < t.map.total(); chunk += gridDim.x) {
     ti = t.map.find(chunk, ti);
     const UnpackEntry& E = t.e[ti];
-    const long long base = (long long)(chunk - t.map.first[ti]) * kChunk + warp * (kUnroll * kGroup8);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const long long i = base + u * kGroup8 + lane * 4, n = E.numel - i;
-      if (n <= 0) continue;
-      const bool vec = t.vec[ti] && n >= 4;
-      const uint32_t mc = load4_codes(E.m, i, n, vec), vc = load4_codes(E.v, i, n, vec);
-      const float ms = E.mscale[i / kGroup8], vs = E.vscale[i / kGroup8];
-      float m[4], v[4];
-      e4m3x4_to_float(mc, m);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        m[e] = __fmul_rn(m[e], ms);
-        const float r = __fmul_rn(root_value((vc >> (8 * e)) & 255u), vs);
-        v[e] = __fmul_rn(r, r);
-      }
-      store4(E.m_out, i, n, vec, GM_F32, m);
-      store4(E.v_out, i, n, vec, GM_F32, v);
-    }
+    const long long base = (long long)(chunk - t.map.first[ti]) * kChunk + warp * kPart;
+    if (t.vec[ti] && base + kPart <= E.numel) unpack_part<true>(E, base + lane * 8);
+    else if (base + lane * 8 < E.numel) unpack_part<false>(E, base + lane * 8);
   }
 }
 
@@ -598,7 +628,7 @@ AdamWKernel pick(int pdt, int gdt) {
 
 cudaError_t launch_adamw_begin(const gm_adamw_params& prm, int64_t* step, const int32_t* skip,
                                void* scratch, cudaStream_t s) {
-  k_adamw_begin<<<1, 1, 0, s>>>(prm.lr, prm.beta1, prm.beta2, prm.wd, prm.clip, prm.lr_dev, skip, step,
+  k_adamw_begin<<<1, 1, 0, s>>>(prm.lr, prm.beta1, prm.beta2, prm.eps, prm.wd, prm.clip, prm.lr_dev, skip, step,
                                 static_cast<Coef*>(scratch));
   return cudaGetLastError();
 }
@@ -606,10 +636,11 @@ cudaError_t launch_adamw_begin(const gm_adamw_params& prm, int64_t* step, const 
 cudaError_t launch_adamw(int count, const gm_adamw_tensor* tensors, int pdt, int gdt, int cdt,
                          const gm_adamw_params& prm, const void* scratch, cudaStream_t s) {
   const Consts k{(float)prm.beta1, (float)(1.0 - prm.beta1), (float)prm.beta2,
-                 (float)(1.0 - prm.beta2), (float)prm.eps, prm.beta1, 1.0 - prm.beta1, prm.beta2,
+                 (float)(1.0 - prm.beta2), (float)prm.eps, (float)sqrt(prm.beta2),
+                 (float)sqrt(1.0 - prm.beta2), prm.beta1, 1.0 - prm.beta1, prm.beta2,
                  1.0 - prm.beta2, cdt};
   const AdamWKernel kernel = prm.bits == 32 ? pick<32>(pdt, gdt) : pick<8>(pdt, gdt);
-  const int state = prm.bits == 32 ? 16 : 4;
+  const int state = prm.bits == 32 ? 32 : 8;   // bytes of eight elements
   for (int at = 0; at < count; at += kMaxTensors) {
     const int n = count - at < kMaxTensors ? count - at : kMaxTensors;
     Table t;
@@ -618,12 +649,16 @@ cudaError_t launch_adamw(int count, const gm_adamw_tensor* tensors, int pdt, int
     for (int i = 0; i < n; ++i) {
       const gm_adamw_tensor& x = tensors[at + i];
       t.e[i] = {x.p, x.g, x.m, x.v, x.mscale, x.vscale, x.copy, x.numel};
-      t.vec[i] = aligned_to(x.p, 4 * width(pdt)) && aligned_to(x.g, 4 * width(gdt)) &&
+      t.vec[i] = aligned_to(x.p, 8 * width(pdt)) && aligned_to(x.g, 8 * width(gdt)) &&
                  aligned_to(x.m, state) && aligned_to(x.v, state) &&
-                 aligned_to(x.copy, 4 * width(cdt));
+                 aligned_to(x.copy, 8 * width(cdt));
     }
     const int total = t.map.first[n];
-    const int grid = total < 4 * sm_count() ? total : 4 * sm_count();   // all resident
+    // 32-bit states: a chunk per CTA, whose launch order walks the arrays front to
+    // back (1e8 elements 410 us, 467 us with resident CTAs that stride); 8-bit states:
+    // resident CTAs, which save a CTA's start per chunk (337 us, 416 us).
+    const int resident = 3 * sm_count();
+    const int grid = prm.bits == 32 || total < resident ? total : resident;
     e = launch_after(kernel, grid, s, t, k, static_cast<const Coef*>(scratch));
     if (e != cudaSuccess) return e;
   }
@@ -639,11 +674,11 @@ cudaError_t launch_adamw_unpack8(int count, const gm_adamw_state8* tensors, cuda
     for (int i = 0; i < n; ++i) {
       const gm_adamw_state8& x = tensors[at + i];
       t.e[i] = {x.m, x.v, x.mscale, x.vscale, x.m_out, x.v_out, x.numel};
-      t.vec[i] = aligned_to(x.m, 4) && aligned_to(x.v, 4) && aligned_to(x.m_out, 16) &&
-                 aligned_to(x.v_out, 16);
+      t.vec[i] = aligned_to(x.m, 8) && aligned_to(x.v, 8) && aligned_to(x.m_out, 32) &&
+                 aligned_to(x.v_out, 32);
     }
     const int total = t.map.first[n];
-    const int grid = total < 8 * sm_count() ? total : 8 * sm_count();
+    const int grid = total;
     k_adamw_unpack8<<<grid, kThreads, 0, s>>>(t);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
