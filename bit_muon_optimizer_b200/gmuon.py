@@ -12,9 +12,11 @@ import contextlib
 import ctypes
 import math
 import os
+import struct
 from dataclasses import dataclass, field
+from itertools import chain
+from operator import attrgetter
 
-import numpy as np
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -709,20 +711,44 @@ class GraspStep:
 
 # ------------------------------------------------- AdamW over lists of tensors
 
+_HERE = contextlib.nullcontext()
+_numel, _get_device, _is_contiguous, _data_ptr, _dtype = (
+    torch.Tensor.numel, torch.Tensor.get_device, torch.Tensor.is_contiguous, torch.Tensor.data_ptr,
+    attrgetter("dtype"))
+
+
 def _on(device):
     """The library works on the current device: makes `device` that, where it is not."""
     if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _HERE
     return torch.cuda.device(device)
 
 
+def _stream_of(device):
+    """The address of torch's current stream on `device` (a stream object costs 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _list_of(tensors, name, dtypes, device=None, numels=None):
-    """Checks a list of non-empty contiguous CUDA tensors on one device."""
+    """Checks a list of non-empty contiguous CUDA tensors on one device; returns the
+    device, the element counts and the set of dtypes."""
     if not isinstance(tensors, (list, tuple)) or not tensors:
         raise ValueError(f"{name}: a non-empty list of tensors expected")
+    dev = tensors[0].device if device is None else device
+    # whole lists at a time: a loop with messages costs a small step more than its kernels
+    counts = list(map(_numel, tensors))
+    kinds = set(map(_dtype, tensors))
+    if not (dev.type == "cuda" and set(map(_get_device, tensors)) == {dev.index} and kinds <= dtypes
+            and all(map(_is_contiguous, tensors))
+            and (0 not in counts if numels is None else counts == numels)):
+        _list_error(tensors, name, dtypes, dev, numels)
+    return dev, counts, kinds
+
+
+def _list_error(tensors, name, dtypes, dev, numels):
+    """The first thing wrong with a list that _list_of refuses."""
     if numels is not None and len(tensors) != len(numels):
         raise ValueError(f"{name}: expected {len(numels)} tensors, got {len(tensors)}")
-    dev = tensors[0].device if device is None else device
     for i, t in enumerate(tensors):
         if t.dtype not in dtypes:
             raise ValueError(f"{name}[{i}]: dtype {t.dtype} is not one of {tuple(dtypes)}")
@@ -733,10 +759,24 @@ def _list_of(tensors, name, dtypes, device=None, numels=None):
         if not t.is_cuda:
             raise ValueError(f"{name}[{i}]: expected a CUDA tensor")
         if t.device != dev:
-            raise ValueError(f"{name}[{i}]: on {t.device}, the others are on {dev}")
+            raise ValueError(f"{name}[{i}]: on {t.device}, expected on {dev}")
         if not t.is_contiguous():
             raise ValueError(f"{name}[{i}]: expected a contiguous tensor")
-    return dev
+    raise ValueError(f"{name}: expected CUDA tensors, got {dev}")
+
+
+_FLOATS = frozenset(_DT)
+_F32 = frozenset((torch.float32,))
+_U8 = frozenset((torch.uint8,))
+
+
+def _rows(*columns):
+    """A host table of int64 rows for the library: entry i of every column."""
+    return struct.pack(f"{len(columns) * len(columns[0])}q", *chain.from_iterable(zip(*columns)))
+
+
+def _addresses(tensors):
+    return list(map(_data_ptr, tensors))
 
 
 def _scalar(t, dtype, name, device):
@@ -763,17 +803,13 @@ def grad_norm(grads, max_norm=None, out=None) -> GradNorm:
     """Norm over all elements of a list of gradients (fp32, bf16, fp16, mixed), and
     min(1, max_norm / (norm + 1e-6)) (1 without ``max_norm``). ``out``: an earlier
     result of a list of at most this length, to write into."""
-    dev = _list_of(grads, "grads", _DT)
+    dev, counts, _ = _list_of(grads, "grads", _FLOATS)
     n = len(grads)
-    table = np.empty((n, 3), dtype=np.int64)
-    table[:, 0] = [t.data_ptr() for t in grads]
-    table[:, 1] = [t.numel() for t in grads]
-    table[:, 2] = [_DT[t.dtype] for t in grads]
+    table = _rows(_addresses(grads), counts, [_DT[t.dtype] for t in grads])
     nb = int(lib.gm_grad_norm_workspace_bytes(n))
     if out is None:
-        buf = torch.empty(256 + nb, dtype=torch.uint8, device=dev)
-        out = GradNorm(buf[8:12].view(torch.float32), buf[0:8].view(torch.float64),
-                       buf[12:16].view(torch.int32), buf[256:])
+        buf = torch.empty(32 + nb // 8, dtype=torch.float64, device=dev)   # ws on 256 bytes
+        out = GradNorm(buf.view(torch.float32)[2:3], buf[:1], buf.view(torch.int32)[3:4], buf[32:])
     else:
         _scalar(out.norm, torch.float32, "out.norm", dev)
         _scalar(out.scale, torch.float64, "out.scale", dev)
@@ -782,9 +818,9 @@ def grad_norm(grads, max_norm=None, out=None) -> GradNorm:
         if out.ws.device != dev:
             raise ValueError(f"out.ws: expected on {dev}, got {out.ws.device}")
     with _on(dev):
-        _check(lib.gm_grad_norm(n, table.ctypes.data, math.inf if max_norm is None else float(max_norm),
-                                _ptr(out.norm), _ptr(out.scale), _ptr(out.status), _ptr(out.ws), nb,
-                                _stream()), "gm_grad_norm")
+        _check(lib.gm_grad_norm(n, table, math.inf if max_norm is None else float(max_norm),
+                                out.norm.data_ptr(), out.scale.data_ptr(), out.status.data_ptr(),
+                                out.ws.data_ptr(), nb, _stream_of(dev)), "gm_grad_norm")
     return out
 
 
@@ -839,13 +875,13 @@ class AdamWState:
 
     def check(self, numels, dev):
         """Raises ValueError unless the state fits tensors of `numels` elements."""
-        kept = (torch.float32,) if self.bits == 32 else (torch.uint8,)
+        kept = _F32 if self.bits == 32 else _U8
         _list_of(self.m, "m", kept, dev, numels)
         _list_of(self.v, "v", kept, dev, numels)
         if self.bits == 8:
             groups = [-(-n // GROUP) for n in numels]
-            _list_of(self.mscale, "mscale", (torch.float32,), dev, groups)
-            _list_of(self.vscale, "vscale", (torch.float32,), dev, groups)
+            _list_of(self.mscale, "mscale", _F32, dev, groups)
+            _list_of(self.vscale, "vscale", _F32, dev, groups)
         _scalar(self.step, torch.int64, "step", dev)
         if self.scratch.device != dev or not self.scratch.is_contiguous():
             raise ValueError(f"scratch: a contiguous tensor on {dev} expected")
@@ -866,14 +902,12 @@ class AdamWState:
             out = tuple([torch.empty(n, dtype=torch.float32, device=dev) for n in numels]
                         for _ in range(2))
         mo, vo = out
-        _list_of(mo, "out[0]", (torch.float32,), dev, numels)
-        _list_of(vo, "out[1]", (torch.float32,), dev, numels)
-        table = np.empty((len(numels), 7), dtype=np.int64)
-        for j, ts in enumerate((self.m, self.v, self.mscale, self.vscale, mo, vo)):
-            table[:, j] = [t.data_ptr() for t in ts]
-        table[:, 6] = numels
+        _list_of(mo, "out[0]", _F32, dev, numels)
+        _list_of(vo, "out[1]", _F32, dev, numels)
+        table = _rows(*map(_addresses, (self.m, self.v, self.mscale, self.vscale, mo, vo)), numels)
         with _on(dev):
-            _check(lib.gm_adamw_unpack8(len(numels), table.ctypes.data, _stream()), "gm_adamw_unpack8")
+            _check(lib.gm_adamw_unpack8(len(numels), table, _stream_of(dev)),
+                   "gm_adamw_unpack8")
         return mo, vo
 
 
@@ -894,12 +928,12 @@ class AdamWStep:
         status makes the call change nothing; ``skip``: such a flag (int32 [1]) alone;
         ``lr``: this step's rate instead of the object's, a number or an fp32 [1]
         tensor on the device (read when the step runs, for captured graphs)."""
-        dev = _list_of(params, "params", _DT)
-        numels = [p.numel() for p in params]
-        _list_of(grads, "grads", _DT, dev, numels)
+        dev, numels, pk = _list_of(params, "params", _FLOATS)
+        _, _, gk = _list_of(grads, "grads", _FLOATS, dev, numels)
         state.check(numels, dev)
+        ck = (torch.float32,)
         if copies is not None:
-            _list_of(copies, "copies", _DT, dev, numels)
+            _, _, ck = _list_of(copies, "copies", _FLOATS, dev, numels)
         if clip is not None:
             if skip is not None:
                 raise ValueError("skip: clip brings its own flag")
@@ -912,37 +946,35 @@ class AdamWStep:
             _scalar(lr, torch.float32, "lr", dev)
             lr_dev, lr = lr.data_ptr(), None
         n = len(numels)
-        table = np.zeros((n, 8), dtype=np.int64)
-        columns = [params, grads, state.m, state.v]
-        if state.bits == 8:
-            columns += [state.mscale, state.vscale]
-        for j, ts in enumerate(columns):
-            table[:, j] = [t.data_ptr() for t in ts]
-        if copies is not None:
-            table[:, 6] = [t.data_ptr() for t in copies]
-        table[:, 7] = numels
-        if len(set(table[:, 0].tolist())) != n or len(set(table[:, 2].tolist())) != n:
+        none = [0] * n
+        columns = [_addresses(params), _addresses(grads), _addresses(state.m), _addresses(state.v),
+                   _addresses(state.mscale) if state.bits == 8 else none,
+                   _addresses(state.vscale) if state.bits == 8 else none,
+                   _addresses(copies) if copies is not None else none, numels]
+        if len(set(columns[0])) != n or len(set(columns[2])) != n:
             raise ValueError("params: a tensor is in the list more than once")
         prm = AdamWParams(self.lr if lr is None else float(lr), *self.betas, self.eps, self.wd,
                           state.bits, clip.scale.data_ptr() if clip is not None else None, lr_dev)
-        kinds = {}
-        for i in range(n):
-            key = (_DT[params[i].dtype], _DT[grads[i].dtype],
-                   _DT[copies[i].dtype] if copies is not None else GM_F32)
-            kinds.setdefault(key, []).append(i)
+        flag = skip.data_ptr() if skip is not None else None
         with _on(dev):
-            s = _stream()
-            if len(kinds) == 1:
-                (key, _), = kinds.items()
-                _check(lib.gm_adamw_step(n, table.ctypes.data, *key, ctypes.byref(prm), _ptr(state.step),
-                                         _ptr(skip), _ptr(state.scratch), s), "gm_adamw_step")
+            s = _stream_of(dev)
+            if len(pk) == len(gk) == len(ck) == 1:
+                table = _rows(*columns)
+                _check(lib.gm_adamw_step(n, table, *[_DT[next(iter(k))] for k in (pk, gk, ck)],
+                                         ctypes.byref(prm), state.step.data_ptr(), flag,
+                                         state.scratch.data_ptr(), s), "gm_adamw_step")
                 return
-            _check(lib.gm_adamw_begin(ctypes.byref(prm), _ptr(state.step), _ptr(skip),
-                                      _ptr(state.scratch), s), "gm_adamw_begin")
-            for key, at in kinds.items():
-                part = np.ascontiguousarray(table[at])
-                _check(lib.gm_adamw_apply(len(at), part.ctypes.data, *key, ctypes.byref(prm),
-                                          _ptr(state.scratch), s), "gm_adamw_apply")
+            kinds = {}
+            for i, row in enumerate(zip(*columns)):
+                kind = (_DT[params[i].dtype], _DT[grads[i].dtype],
+                        _DT[copies[i].dtype] if copies is not None else GM_F32)
+                kinds.setdefault(kind, []).append(row)
+            _check(lib.gm_adamw_begin(ctypes.byref(prm), state.step.data_ptr(), flag,
+                                      state.scratch.data_ptr(), s), "gm_adamw_begin")
+            for kind, rows in kinds.items():
+                table = _rows(*zip(*rows))
+                _check(lib.gm_adamw_apply(len(rows), table, *kind, ctypes.byref(prm),
+                                          state.scratch.data_ptr(), s), "gm_adamw_apply")
 
 
 # ------------------------------------------------ microscaled 4-bit operands
@@ -972,7 +1004,7 @@ class Mx4:
         """An operand's buffers; ``gscale`` to share another operand's (its transpose's)."""
         if fmt not in MX4_BLOCK:
             raise ValueError(f"fmt: GM_MX4 or GM_NV4 expected, got {fmt}")
-        dev = torch.device(device or "cuda")
+        dev = device or torch.device("cuda")
         kp = _mx4_padded(cols)
         if fmt == GM_NV4 and gscale is None:
             gscale = torch.empty(B, dtype=torch.float32, device=dev)
@@ -986,32 +1018,41 @@ class Mx4:
 
     def check(self, name="operand"):
         """Raises ValueError unless the tensors have the operand's layout; returns B."""
+        c, s, g = self.codes, self.scales, self.gscale
+        if self.fmt in MX4_BLOCK and self.rows >= 1 and self.cols >= 1 and c.dim() == 3:
+            B, kp, dev = c.shape[0], _mx4_padded(self.cols), c.get_device()
+            if (c.shape == (B, self.rows, kp // 2) and c.dtype == torch.uint8 and c.is_contiguous() and dev >= 0
+                    and s.shape == (B, -(-self.rows // 128), kp // (4 * MX4_BLOCK[self.fmt]), 32, 4, 4)
+                    and s.dtype == torch.uint8 and s.is_contiguous() and s.get_device() == dev
+                    and (self.fmt == GM_MX4 or g is not None and g.shape == (B,) and g.dtype == torch.float32
+                         and g.is_contiguous() and g.get_device() == dev)):
+                return B
+        self._error(name)
+
+    def _error(self, name):
+        """The first thing wrong with an operand that ``check`` refuses."""
         if self.fmt not in MX4_BLOCK:
             raise ValueError(f"{name}: fmt: GM_MX4 or GM_NV4 expected, got {self.fmt}")
         if self.rows < 1 or self.cols < 1 or self.codes.dim() != 3:
             raise ValueError(f"{name}: codes [B, rows, Kp / 2] of at least one row and column expected")
         B, kp = self.codes.shape[0], _mx4_padded(self.cols)
-        if tuple(self.codes.shape) != (B, self.rows, kp // 2):
-            raise ValueError(f"{name}: codes: expected shape {(B, self.rows, kp // 2)}, "
-                             f"got {tuple(self.codes.shape)}")
-        want = (B, -(-self.rows // 128), kp // (4 * MX4_BLOCK[self.fmt]), 32, 4, 4)
-        if tuple(self.scales.shape) != want:
-            raise ValueError(f"{name}: scales: expected shape {want}, got {tuple(self.scales.shape)}")
-        parts = [("codes", self.codes, torch.uint8), ("scales", self.scales, torch.uint8)]
+        parts = [("codes", self.codes, torch.uint8, (B, self.rows, kp // 2)),
+                 ("scales", self.scales, torch.uint8,
+                  (B, -(-self.rows // 128), kp // (4 * MX4_BLOCK[self.fmt]), 32, 4, 4))]
         if self.fmt == GM_NV4:
-            if self.gscale is None or tuple(self.gscale.shape) != (B,):
+            if self.gscale is None:
                 raise ValueError(f"{name}: gscale: expected shape {(B,)}")
-            parts.append(("gscale", self.gscale, torch.float32))
-        for part, t, dt in parts:
+            parts.append(("gscale", self.gscale, torch.float32, (B,)))
+        for part, t, dt, shape in parts:
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name}: {part}: expected shape {shape}, got {tuple(t.shape)}")
             if t.dtype != dt:
                 raise ValueError(f"{name}: {part}: dtype {t.dtype}, expected {dt}")
             if t.device != self.codes.device:
                 raise ValueError(f"{name}: {part}: on {t.device}, expected on {self.codes.device}")
-            if not t.is_cuda:
-                raise ValueError(f"{name}: {part}: expected a CUDA tensor")
             if not t.is_contiguous():
                 raise ValueError(f"{name}: {part}: expected a contiguous tensor")
-        return B
+        raise ValueError(f"{name}: expected a CUDA tensor")
 
 
 def mx4_quant(X, fmt=GM_MX4, rows=True, cols=False, out=None):
@@ -1055,7 +1096,7 @@ def mx4_quant(X, fmt=GM_MX4, rows=True, cols=False, out=None):
                                 gs.data_ptr() if fmt == GM_NV4 else None,
                                 q.codes.data_ptr() if rows else None, q.scales.data_ptr() if rows else None,
                                 qt.codes.data_ptr() if cols else None,
-                                qt.scales.data_ptr() if cols else None, _stream()), "gm_mx4_quant")
+                                qt.scales.data_ptr() if cols else None, _stream_of(dev)), "gm_mx4_quant")
     return (q, qt) if rows and cols else q if rows else qt
 
 
@@ -1069,9 +1110,9 @@ def mx4_dequant(q: Mx4, out=None, dtype=torch.float32):
     if out.device != dev:
         raise ValueError(f"out: expected on {dev}, got {out.device}")
     with _on(dev):
-        _check(lib.gm_mx4_dequant(B, q.rows, q.cols, q.fmt, _ptr(q.codes), _ptr(q.scales),
-                                  _ptr(q.gscale) if q.fmt == GM_NV4 else None, _ptr(out),
-                                  _DT[out.dtype], _stream()), "gm_mx4_dequant")
+        _check(lib.gm_mx4_dequant(B, q.rows, q.cols, q.fmt, q.codes.data_ptr(), q.scales.data_ptr(),
+                                  q.gscale.data_ptr() if q.fmt == GM_NV4 else None, _ptr(out),
+                                  _DT[out.dtype], _stream_of(dev)), "gm_mx4_dequant")
     return out
 
 
@@ -1095,8 +1136,9 @@ def mx4_matmul(A: Mx4, Bm: Mx4, out_dtype=torch.bfloat16, out=None, accumulate=F
         raise ValueError(f"out: expected on {dev}, got {out.device}")
     nv = A.fmt == GM_NV4
     with _on(dev):
-        _check(lib.gm_mx4_matmul(B, A.rows, Bm.rows, A.cols, A.fmt, _ptr(A.codes), _ptr(A.scales),
-                                 _ptr(A.gscale) if nv else None, _ptr(Bm.codes), _ptr(Bm.scales),
-                                 _ptr(Bm.gscale) if nv else None, _ptr(out), _DT[out.dtype],
-                                 int(bool(accumulate)), _stream()), "gm_mx4_matmul")
+        _check(lib.gm_mx4_matmul(B, A.rows, Bm.rows, A.cols, A.fmt, A.codes.data_ptr(),
+                                 A.scales.data_ptr(), A.gscale.data_ptr() if nv else None,
+                                 Bm.codes.data_ptr(), Bm.scales.data_ptr(),
+                                 Bm.gscale.data_ptr() if nv else None, _ptr(out), _DT[out.dtype],
+                                 int(bool(accumulate)), _stream_of(dev)), "gm_mx4_matmul")
     return out
