@@ -3,15 +3,17 @@
 // (GM_NV4) on packed e2m1 codes with the block scales in tensor memory, sums in
 // fp32, one rounding to D's type.
 //
-// One kernel, two tile shapes:
+// One kernel, two shapes:
 //   CG = 2: a pair of CTAs per 256 x 256 tile (M = 256, N = 256, K = 64 per
 //     instruction), persistent over the tiles. Each CTA loads its 128 rows of A and
 //     128 of the 256 rows of B: per flop the fewest bytes from L2, which bounds the
 //     large products.
-//   CG = 1: one CTA per 128 x 256 tile, and a cluster of up to 8 CTAs that split K and
-//     join their fp32 parts through distributed shared memory in the order of the
-//     ranks (so equal operands give equal bits): for products of few tiles, which
-//     the weight's bytes bound.
+//   CG = 1, for products of few tiles, which B's bytes (a weight's) bound: operands
+//     change places, so that a tile is 128 rows of B (the instruction's M) by up to 256
+//     rows of A (its N, no more than there are, to 16). One CTA per tile, or a cluster of
+//     up to 8 that split K stage by stage and join their fp32 parts through distributed
+//     shared memory in the order of the ranks (so equal operands give equal bits). A lane
+//     holds a column of D, and its stores are contiguous for any N.
 // Roles of a CTA's warps:
 //   warp 0: TMA of A's codes and scales      warp 2: TMA of B's
 //   warp 1: tensor memory; one thread copies a stage's scales to tensor memory
@@ -39,7 +41,8 @@ namespace {
 
 constexpr int kBN = 256;                  // columns of a tile
 constexpr int kStageK = 256;              // columns of K per stage
-constexpr int kStages = 4;
+constexpr int kStages = 4;                // of CG = 2; CG = 1: as many as fit, at most kMaxStages
+constexpr int kMaxStages = 8;
 constexpr int kEpiWarp0 = 4, kEpiWarps = 16;
 constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
 constexpr int kWarpCols = kBN / (kEpiWarps / 4);   // 64 columns of an epilogue warp
@@ -47,31 +50,36 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr int kMaxSplit = 8;              // portable cluster size
 
 constexpr uint32_t kABytes = 128 * (kStageK / 2);
-constexpr uint32_t b_bytes(int cg) { return kBN / cg * (kStageK / 2); }
 constexpr uint32_t sf_bytes(int fmt) { return kStageK / (4 * mx4_block(fmt)) * 512; }   // of 128 rows
-constexpr uint32_t stage_bytes(int cg, int fmt) { return kABytes + b_bytes(cg) + 3 * sf_bytes(fmt); }
+// A stage of a CTA: 128 rows of the first operand, `rows` of the second, the scales of
+// 128 and of `tiles` times 128 rows.
+__host__ __device__ constexpr uint32_t stage_bytes(int fmt, int rows, int tiles) {
+  return kABytes + rows * (kStageK / 2) + (1 + tiles) * sf_bytes(fmt);
+}
 constexpr int kPitch = 17;                // staging of ragged stores: 32 rows x 16 columns a warp
 constexpr uint32_t kStageOut = kEpiWarps * 32 * kPitch * 4;
+constexpr uint32_t ring_bytes(int cg, int fmt) {
+  return kStages * stage_bytes(fmt, cg == 2 ? 128 : kBN, 2);
+}
 constexpr uint32_t smem_bytes(int cg, int fmt) {
-  // a CG = 1 stage ring is 195 to 216 KB: there the ragged staging shares it (the
-  // ring is idle by then only when the CTA has one tile), see ragged_base
-  return kStages * stage_bytes(cg, fmt) + (cg == 2 ? kStageOut : 0) + 1024 /* barriers */ + 1024 /* align */;
+  return ring_bytes(cg, fmt) + (cg == 2 ? kStageOut : 0) + 1024 /* barriers */ + 1024 /* align */;
 }
 static_assert(smem_bytes(1, GM_NV4) <= 227 * 1024 && smem_bytes(2, GM_NV4) <= 227 * 1024, "shared memory");
-constexpr int kPartPitch = kBN + 4;       // fp32 part of a split tile, 16-byte rows without conflicts
-static_assert(128 * kPartPitch * 4 <= kStages * stage_bytes(1, GM_MX4), "a part fits the idle ring");
+static_assert(kBN * 128 * 4 <= ring_bytes(1, GM_MX4), "a part of a split tile fits the idle ring");
 
-// Tensor memory columns: accumulator, then per stage the scales of A and of B (4
-// columns per atom of 128 rows).
+// Tensor memory columns: the accumulator, then per stage the scales of the first and of
+// the second operand (4 columns per atom of 128 rows).
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t sf_cols(int fmt) { return sf_bytes(fmt) / 128; }   // of 128 rows, one stage
-constexpr uint32_t tmem_sfa(int fmt, int s) { return kBN + s * 3 * sf_cols(fmt); }
-constexpr uint32_t tmem_sfb(int fmt, int s) { return tmem_sfa(fmt, s) + sf_cols(fmt); }
-static_assert(tmem_sfa(GM_NV4, kStages) <= kTmemCols, "tensor memory");
+__host__ __device__ constexpr uint32_t sf_cols(int fmt) { return sf_bytes(fmt) / 128; }   // of 128 rows, one stage
+static_assert(kBN + kStages * 3 * sf_cols(GM_NV4) <= kTmemCols && kBN + kMaxStages * 2 * sf_cols(GM_NV4) <= kTmemCols,
+              "tensor memory");
 
 struct ProductParams {
   int M, N, K;
   int batch, tiles_m, tiles_n;
+  int bn;                  // columns of a tile's accumulator (CG = 1: 16 .. 256, CG = 2: 256)
+  int sf_tiles;            // 128-row tiles of the second operand's scales in a stage
+  int stages;
   int split;               // CTAs that share a tile's K (CG = 1)
   void* D;
   int ddt, accumulate;
@@ -115,28 +123,32 @@ __device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* map, ui
 // One scale atom (512 bytes, rows of 16) to four columns of tensor memory, in both
 // CTAs of a pair.
 template <int CG>
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
+__device__ __forceinline__ void copy_scales(uint32_t one, uint32_t tmem, uint32_t smem) {
   // no swizzle; 128 bytes from one group of eight 16-byte rows to the next
   const uint64_t d = (uint64_t)((smem >> 4) & 0x3FFF) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
   if constexpr (CG == 2)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+                 "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}\n" ::"r"(tmem), "l"(d), "r"(one)
+                 : "memory");
   else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+                 "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}\n" ::"r"(tmem), "l"(d), "r"(one)
+                 : "memory");
 }
 // Instruction descriptor of the block-scaled 4-bit kinds: e2m1 operands, K-major, K =
 // 64; `sf` selects the scale bytes of a 32-bit word to begin with.
 template <int CG, int FMT>
-__host__ __device__ constexpr uint32_t idesc_mx4(uint32_t sf) {
-  return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kBN >> 3) << 17) |
+__host__ __device__ constexpr uint32_t idesc_mx4(uint32_t sf, int n) {
+  return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) |
          ((FMT == GM_MX4 ? 1u : 0u) << 23) | ((uint32_t)(128 * CG >> 7) << 27) | (sf << 29);
 }
 template <int CG, int FMT>
-__device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+__device__ __forceinline__ void umma_mx4(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                          uint32_t sfb, uint32_t accumulate) {
 #define GM_UMMA_MX4(GROUP, KIND)                                                                   \
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                   \
-               "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d), \
-               "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                     \
+  asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 e, %7, 0;\n\t"        \
+               "@e tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d), \
+               "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(one)           \
                : "memory")
   if constexpr (CG == 2 && FMT == GM_MX4) GM_UMMA_MX4("2", "mxf4.block_scale.scale_vec::2X");
   if constexpr (CG == 2 && FMT == GM_NV4) GM_UMMA_MX4("2", "mxf4nvf4.block_scale.scale_vec::4X");
@@ -144,12 +156,27 @@ __device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t a, uint64_t b, uin
   if constexpr (CG == 1 && FMT == GM_NV4) GM_UMMA_MX4("1", "mxf4nvf4.block_scale.scale_vec::4X");
 #undef GM_UMMA_MX4
 }
+// Arrive on the barrier (of both CTAs of a pair) once the MMAs issued so far are done.
 template <int CG>
-__device__ __forceinline__ void commit(uint32_t bar) {
+__device__ __forceinline__ void commit(uint32_t one, uint32_t bar) {
   if constexpr (CG == 2)
-    umma_commit_pair(bar);
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+                 "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+                 " [%0], %1;\n\t}\n" ::"r"(bar), "h"((uint16_t)3), "r"(one)
+                 : "memory");
   else
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar),
+                 "r"(one)
+                 : "memory");
+}
+// One lane of a converged warp. The instructions below are issued by it under a
+// predicate, the warp staying together: their operands then live in uniform
+// registers (under a branch each tcgen05 instruction took about 55 ns to issue).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}\n" : "=r"(r));
+  return r;
 }
 // 64 columns of 32 lanes of tensor memory.
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
@@ -259,15 +286,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_mx4_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                const ProductParams p) {
-  constexpr uint32_t kSf = sf_bytes(FMT), kStage = stage_bytes(CG, FMT), kB = b_bytes(CG);
+  constexpr uint32_t kSf = sf_bytes(FMT);
   constexpr int kAtoms = kSf / 512;
+  // constants for CG = 2
+  const int bn = CG == 2 ? kBN : p.bn, sft = CG == 2 ? 2 : p.sf_tiles;
+  const uint32_t stages = CG == 2 ? kStages : (uint32_t)p.stages;
+  const uint32_t b_size = (uint32_t)(bn / CG) * (kStageK / 2), stage = stage_bytes(FMT, bn / CG, sft);
   extern __shared__ __align__(1024) uint8_t dsm[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm) + 1023) & ~uintptr_t(1023));
-  uint8_t* after = ring + kStages * kStage;
-  float* stage_out = reinterpret_cast<float*>(CG == 2 ? after : ring);
+  uint8_t* after = ring + ring_bytes(CG, FMT);
+  float* stage_out = reinterpret_cast<float*>(after);            // CG = 2
   uint64_t* full = reinterpret_cast<uint64_t*>(after + (CG == 2 ? kStageOut : 0));
-  uint64_t* empty = full + kStages;
-  uint64_t* acc_full = empty + kStages;
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* acc_full = empty + kMaxStages;
   uint64_t* acc_empty = acc_full + 1;
   uint64_t* drain = acc_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -276,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* consumed = flags + 1;
   int* issued = flags + 2;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int group = CG == 2 ? 2 : p.split;                  // CTAs of a cluster
   const bool leader = CG == 1 || rank == 0;                 // issues MMAs
@@ -284,12 +315,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tiles = p.tiles_m * p.tiles_n, total = p.batch * tiles;
   const int k64 = (int)(mx4_padded(p.K) / 64);              // instructions along K
   const int nst = cdiv(k64, kStageK / 64);
-  const int st0 = CG == 1 ? (int)((long long)nst * rank / p.split) : 0;
-  const int st1 = CG == 1 ? (int)((long long)nst * (rank + 1) / p.split) : nst;
-  constexpr uint32_t kStageTx = CG * kStage;
+  // CG = 1: the ranks of a cluster take turns, so that together they read a row's bytes
+  // in order
+  const int st0 = CG == 1 ? (int)rank : 0, st_step = CG == 1 ? p.split : 1;
+  const uint32_t stage_tx = CG * stage;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < (int)stages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
@@ -321,13 +353,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (group > 1) cluster_sync_all();   // barriers initialised before any signal from another CTA
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
+  // First row of this CTA's part of a tile in the instruction's first operand (CG = 2: A,
+  // CG = 1: B) and in its second.
   auto origin = [&](int T, int& bz, int& r0, int& c0) {
     bz = T / tiles;
     const int x = T - bz * tiles;
-    r0 = (x % p.tiles_m) * (128 * CG) + (CG == 2 ? (int)rank * 128 : 0);
-    c0 = x / p.tiles_m * kBN;
+    if constexpr (CG == 2) {
+      r0 = x % p.tiles_m * 256 + (int)rank * 128;
+      c0 = x / p.tiles_m * kBN;
+    } else {
+      r0 = x % p.tiles_n * 128;
+      c0 = x / p.tiles_n * bn;
+    }
+  };
+  auto slot = [&](uint32_t g, uint32_t& s, uint32_t& ph) {
+    s = g % stages;
+    ph = (g / stages) & 1u;
   };
 
   if (warp == 0 || warp == 2) {
@@ -339,13 +382,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int T = cid; T < total && ok; T += ncl) {
         int bz, r0, c0;
         origin(T, bz, r0, c0);
-        for (int st = st0; st < st1; ++st, ++g) {
-          const int s = (int)(g % kStages);
-          if (!mbar_wait(smem_u32(&empty[s]), ((g / kStages) & 1u) ^ 1u, p.err, abort_flag, kWaitLimitNs)) { ok = false; break; }
+        for (int st = st0; st < nst; st += st_step, ++g) {
+          uint32_t s, ph;
+          slot(g, s, ph);
+          if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1u, p.err, abort_flag, kWaitLimitNs)) { ok = false; break; }
           const uint32_t bar = CG == 2 ? map_to_rank(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
-          const uint32_t a = smem_u32(ring + s * kStage), b = a + kABytes, sa = b + kB, sb = sa + kSf;
+          const uint32_t a = smem_u32(ring + s * stage), b = a + kABytes, sa = b + b_size, sb = sa + kSf;
           if (isA) {
-            if (leader) mbar_expect_tx(smem_u32(&full[s]), kStageTx);
+            if (leader) mbar_expect_tx(smem_u32(&full[s]), stage_tx);
             load_3d<CG>(a, &tmA, bar, st * (kStageK / 2), r0, bz);
             load_4d<CG>(sa, &tmSA, bar, 0, st * kAtoms, r0 / 128, bz);
           } else {
@@ -357,26 +401,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       atomicMax(issued, (int)g);
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      // ---------------- MMA issuer
+    if (leader) {
+      // ---------------- MMA issuer: the whole warp, instructions from one lane
+      const uint32_t one = elect_one();
       uint32_t g = 0;
       bool ok = true;
       int it = 0;
       for (int T = cid; T < total && ok; T += ncl, ++it) {
-        if (!mbar_wait(smem_u32(acc_empty), ((uint32_t)it & 1u) ^ 1u, p.err, abort_flag, kWaitLimitNs)) { ok = false; break; }
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(acc_empty), ((uint32_t)it & 1u) ^ 1u, p.err, abort_flag, kWaitLimitNs));
+        if (!ok) break;
         tc_fence_after();
-        for (int st = st0; st < st1; ++st, ++g) {
-          const int s = (int)(g % kStages);
-          if (!mbar_wait(smem_u32(&full[s]), (g / kStages) & 1u, p.err, abort_flag, kWaitLimitNs)) { ok = false; break; }
+        for (int st = st0; st < nst; st += st_step, ++g) {
+          uint32_t s, ph;
+          slot(g, s, ph);
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), ph, p.err, abort_flag, kWaitLimitNs));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a = smem_u32(ring + s * kStage), b = a + kABytes, sa = b + kB, sb = sa + kSf;
-          const uint32_t ta = tmem + tmem_sfa(FMT, s), tb = tmem + tmem_sfb(FMT, s);
+          const uint32_t a = smem_u32(ring + s * stage), b = a + kABytes, sa = b + b_size, sb = sa + kSf;
+          const uint32_t ta = tmem + kBN + s * (uint32_t)(1 + sft) * sf_cols(FMT), tb = ta + sf_cols(FMT);
 #pragma unroll
           for (int j = 0; j < kAtoms; ++j) {
-            copy_scales<CG>(ta + j * 4, sa + j * 512);
-            // B: [128-row tile][atom] in shared memory, [atom][tile] in tensor memory
-            copy_scales<CG>(tb + j * 8, sb + j * 512);
-            copy_scales<CG>(tb + j * 8 + 4, sb + kSf + j * 512);
+            copy_scales<CG>(one, ta + j * 4, sa + j * 512);
+            // second operand: [128-row tile][atom] in shared memory, [atom][tile] in tensor memory
+            copy_scales<CG>(one, tb + j * 4 * sft, sb + j * 512);
+            if (sft == 2) copy_scales<CG>(one, tb + j * 8 + 4, sb + kSf + j * 512);
           }
 #pragma unroll
           for (int kk = 0; kk < kStageK / 64; ++kk) {
@@ -384,51 +432,76 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (k >= k64) break;
             const int j = kk * kAtoms / (kStageK / 64);          // the atom that holds this k
             const uint32_t sf = FMT == GM_MX4 ? (kk & 1) * 2 : 0;
-            umma_mx4<CG, FMT>(tmem, sdesc(a + kk * 32, 16, 1024), sdesc(b + kk * 32, 16, 1024),
-                              idesc_mx4<CG, FMT>(sf), ta + j * 4, tb + j * 8, (st > st0 || kk) ? 1u : 0u);
+            umma_mx4<CG, FMT>(one, tmem, sdesc(a + kk * 32, 16, 1024), sdesc(b + kk * 32, 16, 1024),
+                              idesc_mx4<CG, FMT>(sf, bn), ta + j * 4, tb + j * 4 * sft, (st > st0 || kk) ? 1u : 0u);
           }
-          commit<CG>(smem_u32(&empty[s]));
+          commit<CG>(one, smem_u32(&empty[s]));
         }
         if (!ok) break;
-        commit<CG>(smem_u32(acc_full));
+        commit<CG>(one, smem_u32(acc_full));
       }
-      *consumed = (int)g;
-      if (!ok) *abort_flag = 1;
-      commit<CG>(smem_u32(drain));       // fires once every MMA issued above has completed
+      if (lane == 0) {
+        *consumed = (int)g;
+        if (!ok) *abort_flag = 1;
+      }
+      commit<CG>(one, smem_u32(drain));       // fires once every MMA issued above has completed
       mbar_wait(smem_u32(drain), 0, p.err, nullptr, kWaitLimitNs);
     }
   } else if (warp >= kEpiWarp0) {
     // ---------------- epilogue
-    const int q = warp & 3, part = (warp - kEpiWarp0) >> 2;     // lane quarter, 64-column part
-    const uint32_t bar = CG == 2 ? map_to_rank(smem_u32(acc_empty), 0) : smem_u32(acc_empty);
-    int it = 0;
-    for (int T = cid; T < total; T += ncl, ++it) {
-      int bz, r0, c0;
-      origin(T, bz, r0, c0);
-      const float alpha = FMT == GM_NV4 ? p.ag[bz] * p.bg[bz] : 1.f;
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(acc_full), (uint32_t)it & 1u, p.err, abort_flag, kWaitLimitNs))) break;
-      tc_fence_after();
-      float v[64];
-      tmem_ld64(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(part * kWarpCols), v);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0)
-        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-      const int c = c0 + part * kWarpCols;
-      if (FMT == GM_NV4 && group == CG) {
+    const int q = warp & 3, part = (warp - kEpiWarp0) >> 2;     // lane quarter, column part
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    if constexpr (CG == 2) {
+      const uint32_t bar = map_to_rank(smem_u32(acc_empty), 0);
+      int it = 0;
+      for (int T = cid; T < total; T += ncl, ++it) {
+        int bz, r0, c0;
+        origin(T, bz, r0, c0);
+        const float alpha = FMT == GM_NV4 ? p.ag[bz] * p.bg[bz] : 1.f;
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(acc_full), (uint32_t)it & 1u, p.err, abort_flag, kWaitLimitNs))) break;
+        tc_fence_after();
+        float v[64];
+        tmem_ld64(lanes + (uint32_t)(part * kWarpCols), v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+        const int c = c0 + part * kWarpCols;
+        if (FMT == GM_NV4) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) v[e] *= alpha;
-      }
-      if (CG == 1 && group > 1) {
-        // this rank's fp32 part of the tile, in the idle ring
-        float* part_row = reinterpret_cast<float*>(ring) + (q * 32 + lane) * kPartPitch + part * kWarpCols;
-        if (r0 + q * 32 + lane < p.M) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            *reinterpret_cast<float4*>(part_row + 4 * e) = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          for (int e = 0; e < 64; ++e) v[e] *= alpha;
         }
-      } else if (c < p.N) {
-        store_warp(p, v, bz, r0 + q * 32, c, lane, stage_out + (warp - kEpiWarp0) * 32 * kPitch);
+        if (c < p.N) store_warp(p, v, bz, r0 + q * 32, c, lane, stage_out + (warp - kEpiWarp0) * 32 * kPitch);
+      }
+    } else {
+      int bz, r0, c0;
+      origin(cid, bz, r0, c0);
+      const float alpha = FMT == GM_NV4 ? p.ag[bz] * p.bg[bz] : 1.f;
+      const int n = r0 + q * 32 + lane;                         // this lane's column of D
+      if (__all_sync(0xffffffffu, mbar_wait(smem_u32(acc_full), 0, p.err, abort_flag, kWaitLimitNs))) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int ch = part; ch * 16 < bn && c0 + ch * 16 < p.M; ch += kEpiWarps / 4) {
+          float v[16];
+          tmem_ld16(lanes + (uint32_t)(ch * 16), v);
+          const int rows = p.M - (c0 + ch * 16);
+          if (group > 1) {
+            // this rank's fp32 part of the tile, [row of D][128 columns], in the idle ring
+            float* to = reinterpret_cast<float*>(ring) + ch * 16 * 128 + q * 32 + lane;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e < rows) to[e * 128] = v[e];
+          } else if (n < p.N) {
+            const long long at = ((long long)bz * p.M + c0 + ch * 16) * p.N + n;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              if (e >= rows) break;
+              float d = FMT == GM_NV4 ? v[e] * alpha : v[e];
+              if (p.accumulate) d += load_as_float(p.D, at + (long long)e * p.N, p.ddt);
+              store_from_float(p.D, at + (long long)e * p.N, p.ddt, d);
+            }
+          }
+        }
       }
     }
   }
@@ -436,46 +509,53 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (threadIdx.x == 0 && leader) {
     // after an abort, let the copies still in flight land
-    for (int g = *consumed; g < *issued; ++g)
-      mbar_wait(smem_u32(&full[g % kStages]), (uint32_t)(g / kStages) & 1u, p.err, nullptr, kWaitLimitNs);
+    for (int g = *consumed; g < *issued; ++g) {
+      uint32_t s, ph;
+      slot((uint32_t)g, s, ph);
+      mbar_wait(smem_u32(&full[s]), ph, p.err, nullptr, kWaitLimitNs);
+    }
   }
   if (group > 1) cluster_sync_all();
   if (CG == 1 && group > 1) {
-    // join the parts: vector i of the tile's valid rows belongs to rank i mod split
+    // join the parts: rank r takes every group-th run of four columns
     int bz, r0, c0;
     origin(cid, bz, r0, c0);
     const float alpha = FMT == GM_NV4 ? p.ag[bz] * p.bg[bz] : 1.f;
-    const int rows = min(128, p.M - r0), cols = min(kBN, p.N - c0);
+    const int rows = min(bn, p.M - c0);
     const uint32_t mine = smem_u32(ring);
     uint32_t remote[kMaxSplit];
 #pragma unroll
     for (int r = 0; r < kMaxSplit; ++r) remote[r] = r < group ? map_to_rank(mine, r) : 0u;
-    for (int i = threadIdx.x * group + (int)rank; i < rows * (kBN / 4); i += kThreads * group) {
-      const int r = i / (kBN / 4), c = i % (kBN / 4) * 4;
-      if (c >= cols) continue;
+    for (int i = threadIdx.x * group + (int)rank; i < rows * 32; i += kThreads * group) {
+      const int r = i / 32, n = r0 + i % 32 * 4;
+      if (n >= p.N) continue;
+      float4 x[kMaxSplit];   // all loads first: each takes most of a microsecond
+#pragma unroll
+      for (int s = 0; s < kMaxSplit; ++s) {
+        x[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s < group)
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(x[s].x), "=f"(x[s].y), "=f"(x[s].z), "=f"(x[s].w)
+                       : "r"(remote[s] + (uint32_t)i * 16)
+                       : "memory");
+      }
       float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < kMaxSplit; ++s) {
-        if (s >= group) break;
-        float4 x;
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                     : "r"(remote[s] + (uint32_t)((r * kPartPitch + c) * 4))
-                     : "memory");
-        o[0] += x.x; o[1] += x.y; o[2] += x.z; o[3] += x.w;
+        o[0] += x[s].x; o[1] += x[s].y; o[2] += x[s].z; o[3] += x[s].w;
       }
-      const long long at = ((long long)bz * p.M + r0 + r) * p.N + c0 + c;
+      const long long at = ((long long)bz * p.M + c0 + r) * p.N + n;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (FMT == GM_NV4) o[e] *= alpha;
-        if (p.accumulate && c + e < cols) o[e] += load_as_float(p.D, at + e, p.ddt);
+        if (p.accumulate && n + e < p.N) o[e] += load_as_float(p.D, at + e, p.ddt);
       }
       if (p.N % 4 == 0) {
         store4_from_float(p.D, at, p.ddt, make_float4(o[0], o[1], o[2], o[3]));
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (c + e < cols) store_from_float(p.D, at + e, p.ddt, o[e]);
+          if (n + e < p.N) store_from_float(p.D, at + e, p.ddt, o[e]);
       }
     }
     cluster_sync_all();   // no CTA leaves while another still reads its part
@@ -556,19 +636,29 @@ cudaError_t launch_mx4_matmul(int B, int M, int N, int K, int fmt, const uint8_t
   p.ag = ag; p.bg = bg;
   p.err = device_error_word();
   if (!p.err) return cudaErrorUnknown;
-  p.tiles_n = cdiv(N, kBN);
-  const bool pair = (long long)cdiv(M, 256) * p.tiles_n * B >= sm_count() / 4;
-  p.tiles_m = cdiv(M, pair ? 256 : 128);
+  const bool pair = (long long)cdiv(M, 256) * cdiv(N, kBN) * B >= sm_count() / 4;
   p.split = 1;
-  if (!pair) {
+  Maps m;
+  bool ok;
+  if (pair) {
+    p.tiles_m = cdiv(M, 256);
+    p.tiles_n = cdiv(N, kBN);
+    ok = map_codes(&m.A, a, B, M, K, 128) && map_codes(&m.B, b, B, N, K, 128) &&
+         map_scales(&m.SA, as, B, M, K, fmt, 1) && map_scales(&m.SB, bs, B, N, K, fmt, 2);
+  } else {
+    p.bn = M < kBN ? cdiv(M, 16) * 16 : kBN;
+    p.sf_tiles = cdiv(p.bn, 128);
+    const uint32_t fit = ring_bytes(1, fmt) / stage_bytes(fmt, p.bn, p.sf_tiles);
+    p.stages = p.sf_tiles == 2 ? kStages : (int)(fit < kMaxStages ? fit : kMaxStages);
+    p.tiles_m = cdiv(M, p.bn);
+    p.tiles_n = cdiv(N, 128);
     const long long tiles = (long long)p.tiles_m * p.tiles_n * B;
     const int nst = cdiv((int)(mx4_padded(K) / 64), kStageK / 64);
     while (p.split < kMaxSplit && tiles * p.split * 2 <= sm_count() && nst >= 4 * p.split) p.split *= 2;
+    ok = map_codes(&m.A, b, B, N, K, 128) && map_codes(&m.B, a, B, M, K, p.bn) &&
+         map_scales(&m.SA, bs, B, N, K, fmt, 1) && map_scales(&m.SB, as, B, M, K, fmt, p.sf_tiles);
   }
-  Maps m;
-  if (!map_codes(&m.A, a, B, M, K, 128) || !map_codes(&m.B, b, B, N, K, pair ? 128 : 256) ||
-      !map_scales(&m.SA, as, B, M, K, fmt, 1) || !map_scales(&m.SB, bs, B, N, K, fmt, 2))
-    return cudaErrorInvalidValue;
+  if (!ok) return cudaErrorInvalidValue;
   if (fmt == GM_MX4) return pair ? launch_t<2, GM_MX4>(m, p, s) : launch_t<1, GM_MX4>(m, p, s);
   return pair ? launch_t<2, GM_NV4>(m, p, s) : launch_t<1, GM_NV4>(m, p, s);
 }
