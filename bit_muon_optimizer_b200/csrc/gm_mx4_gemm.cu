@@ -636,7 +636,7 @@ cudaError_t launch_mx4_matmul(int B, int M, int N, int K, int fmt, const uint8_t
   p.ag = ag; p.bg = bg;
   p.err = device_error_word();
   if (!p.err) return cudaErrorUnknown;
-  const bool pair = (long long)cdiv(M, 256) * cdiv(N, kBN) * B >= sm_count() / 4;
+  const bool pair = M > 128 && (long long)cdiv(M, 256) * cdiv(N, kBN) * B >= sm_count() / 4;
   p.split = 1;
   Maps m;
   bool ok;
@@ -654,7 +654,9 @@ cudaError_t launch_mx4_matmul(int B, int M, int N, int K, int fmt, const uint8_t
     p.tiles_n = cdiv(N, 128);
     const long long tiles = (long long)p.tiles_m * p.tiles_n * B;
     const int nst = cdiv((int)(mx4_padded(K) / 64), kStageK / 64);
-    while (p.split < kMaxSplit && tiles * p.split * 2 <= sm_count() && nst >= 4 * p.split) p.split *= 2;
+    // A join costs about 2 us and a quarter of a stage's time per eight rows; a split
+    // halves the stages.
+    while (p.split < kMaxSplit && tiles * p.split * 2 <= sm_count() && nst >= (8 + p.bn / 8) * p.split) p.split *= 2;
     ok = map_codes(&m.A, b, B, N, K, 128) && map_codes(&m.B, a, B, M, K, p.bn) &&
          map_scales(&m.SA, bs, B, N, K, fmt, 1) && map_scales(&m.SB, as, B, M, K, fmt, p.sf_tiles);
   }
