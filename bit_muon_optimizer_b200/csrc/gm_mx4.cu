@@ -25,28 +25,69 @@ constexpr int kThreads = 256;
 constexpr int kTile = 128;
 constexpr int kRowSpan = 1024;   // elements of a row that a warp takes at a time
 
-// Eight consecutive elements from column c of a row of n (zeros behind its end).
+// ------------------------------------------------------------------- elements
+// Eight consecutive elements of a row as they lie in memory.
 template <int DT>
-__device__ __forceinline__ void load8(const void* row, long long c, long long n, bool vec, float (&o)[8]) {
+struct Eight {
+  uint32_t w[DT == GM_F32 ? 8 : 4];
+};
+// From column c of a row of n (zeros behind its end).
+template <int DT>
+__device__ __forceinline__ void load8(const void* row, long long c, long long n, bool vec, Eight<DT>& x) {
   if (vec && c + 8 <= n) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + c * (DT == GM_F32 ? 4 : 2));
+    const uint4 a = p[0];
+    x.w[0] = a.x; x.w[1] = a.y; x.w[2] = a.z; x.w[3] = a.w;
     if constexpr (DT == GM_F32) {
-      const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + c);
-      const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + c + 4);
-      o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-      o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
-    } else {
-      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        o[2 * j] = h16_to_float((uint16_t)(w[j] & 0xFFFFu), DT == GM_F16);
-        o[2 * j + 1] = h16_to_float((uint16_t)(w[j] >> 16), DT == GM_F16);
-      }
+      const uint4 b = p[1];
+      x.w[4] = b.x; x.w[5] = b.y; x.w[6] = b.z; x.w[7] = b.w;
     }
+  } else if constexpr (DT == GM_F32) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x.w[e] = c + e < n ? static_cast<const uint32_t*>(row)[c + e] : 0u;
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(row);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      x.w[j] = (c + 2 * j < n ? (uint32_t)p[c + 2 * j] : 0u) | (c + 2 * j + 1 < n ? (uint32_t)p[c + 2 * j + 1] << 16 : 0u);
+  }
+}
+template <int DT>
+__device__ __forceinline__ float lo_half(uint32_t w) {
+  return DT == GM_BF16 ? __uint_as_float(w << 16) : __half2float(__ushort_as_half((uint16_t)(w & 0xFFFFu)));
+}
+template <int DT>
+__device__ __forceinline__ float hi_half(uint32_t w) {
+  return DT == GM_BF16 ? __uint_as_float(w & 0xFFFF0000u) : __half2float(__ushort_as_half((uint16_t)(w >> 16)));
+}
+template <int DT>
+__device__ __forceinline__ void to_floats(const Eight<DT>& x, float (&o)[8]) {
+  if constexpr (DT == GM_F32) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = __uint_as_float(x.w[e]);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = c + e < n ? load_as_float(row, c + e, DT) : 0.f;
+    for (int j = 0; j < 4; ++j) {
+      o[2 * j] = lo_half<DT>(x.w[j]);
+      o[2 * j + 1] = hi_half<DT>(x.w[j]);
+    }
   }
+}
+// Magnitudes are compared as unsigned bits, two 16-bit ones at a time: ordered like
+// the values, a NaN above all of them.
+template <int DT>
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t t, uint32_t w) {
+  if constexpr (DT == GM_F32) return max(t, w & 0x7FFFFFFFu);
+  else return __vmaxu2(t, w & 0x7FFF7FFFu);
+}
+// fp32 bits of the largest magnitude of eight.
+template <int DT>
+__device__ __forceinline__ uint32_t top8(const Eight<DT>& x) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int j = 0; j < (DT == GM_F32 ? 8 : 4); ++j) t = max_magnitude<DT>(t, x.w[j]);
+  if constexpr (DT == GM_F32) return t;
+  else return __float_as_uint(lo_half<DT>(max(t & 0xFFFFu, t >> 16)));
 }
 
 // --------------------------------------------------------------------- encoding
@@ -130,10 +171,10 @@ __device__ __forceinline__ uint32_t block_scale(float top, const MatrixScale& g,
 
 // Codes of eight elements under sb gs: |x| against border * sb * gs, a product of at
 // most 31 bits, exact in fp64.
-struct Eight {
+struct Values {
   float x[8];
 };
-__device__ __noinline__ uint32_t exact_codes(Eight v, float sb, float gs) {
+__device__ __noinline__ uint32_t exact_codes(Values v, float sb, float gs) {
   const double s = (double)sb * (double)gs;
   uint32_t w = 0;
 #pragma unroll
@@ -167,16 +208,9 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8], uint32_t b, floa
     }
     uint32_t w = e2m1x8(y);
     if (w != e2m1x8(z) || g.exact)
-      w = exact_codes(Eight{x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]}, e4m3_value(b), g.gs);
+      w = exact_codes(Values{x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]}, e4m3_value(b), g.gs);
     return w;
   }
-}
-
-__device__ __forceinline__ uint32_t top8(const float (&x)[8]) {
-  uint32_t a = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(fabsf(x[e])));
-  return a;
 }
 
 struct QuantParams {
@@ -208,9 +242,12 @@ __global__ void __launch_bounds__(kThreads) k_mx4_top(const QuantParams p) {
   const long long spans = cdivll(p.n, kRowSpan), items = spans * p.m;
   for (long long i = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < items;
        i += (long long)gridDim.x * (kThreads / 32)) {
-    const long long r = i / spans, c0 = (i - r * spans) * kRowSpan;
+    long long r;
+    if (items < (1LL << 31)) r = (uint32_t)i / (uint32_t)spans;   // a 64-bit division costs more than the loads
+    else r = i / spans;
+    const long long c0 = (i - r * spans) * kRowSpan;
     const void* row = row_ptr(p, b, r, kElem<DT>);
-    float x[kRowSpan / 256][8];
+    Eight<DT> x[kRowSpan / 256];
 #pragma unroll
     for (int u = 0; u < kRowSpan / 256; ++u) load8<DT>(row, c0 + u * 256 + lane * 8, p.n, p.vec != 0, x[u]);
 #pragma unroll
@@ -245,7 +282,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_rows(const QuantParams p, long
   const MatrixScale g = matrix_scale<FMT>(p.gscale, b);
   const void* row = row_ptr(p, b, live ? r : 0, kElem<DT>);
   const long long n = live ? p.n : 0;
-  float x[kRowSpan / 256][8];
+  Eight<DT> x[kRowSpan / 256];
 #pragma unroll
   for (int u = 0; u < kRowSpan / 256; ++u)
     load8<DT>(row, c0 + u * 256 + lane * 8, n, p.vec != 0, x[u]);
@@ -257,9 +294,11 @@ __global__ void __launch_bounds__(kThreads) k_mx4_rows(const QuantParams p, long
     for (int o = 1; o < L; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     float mul;
     const uint32_t s = block_scale<FMT>(__uint_as_float(top), g, mul);
-    if (live && c < np)
-      *reinterpret_cast<uint32_t*>(p.codes + ((b * (long long)p.m + r) * np + c) / 2) =
-          codes8<FMT>(x[u], s, mul, g);
+    if (live && c < np) {
+      float v[8];
+      to_floats<DT>(x[u], v);
+      *reinterpret_cast<uint32_t*>(p.codes + ((b * (long long)p.m + r) * np + c) / 2) = codes8<FMT>(v, s, mul, g);
+    }
     // lane 4 L i gathers the bytes of lanes 4 L i, + L, + 2 L, + 3 L
     uint32_t w = s;
     w |= __shfl_down_sync(0xffffffffu, s, L) << 8;
@@ -272,95 +311,108 @@ __global__ void __launch_bounds__(kThreads) k_mx4_rows(const QuantParams p, long
 
 // ----------------------------------------------------------------- both or columns
 // A CTA takes a 128 x 128 tile. Each thread loads eight elements of a row at a time,
-// quantises them along the row, and leaves them in shared memory (16-bit inputs as
-// they are); then it takes two neighbouring columns of 32 rows. Scale bytes of both
+// quantises them along the row, and leaves them in shared memory as they are; then it
+// takes two neighbouring columns of 32 rows. Scale bytes of both
 // orientations are gathered in shared memory and leave as whole atoms.
-template <int DT>
-struct TileType { using T = uint16_t; };
-template <>
-struct TileType<GM_F32> { using T = float; };
-
 template <int DT, int FMT>
 __global__ void __launch_bounds__(kThreads) k_mx4_tile(const QuantParams p) {
-  using T = typename TileType<DT>::T;
   constexpr int BL = mx4_block(FMT), L = BL / 8, NA = kTile / (4 * BL);   // atoms of a tile: 1 or 2
-  extern __shared__ __align__(16) uint8_t dyn[];
-  T* tile = reinterpret_cast<T*>(dyn);
+  constexpr int W = DT == GM_F32 ? 8 : 4;                                 // words of eight elements
+  extern __shared__ __align__(16) uint32_t tile[];                        // [kTile][kTile elements]
   __shared__ __align__(16) uint8_t sR[NA * 512], sC[NA * 512];
   const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long tm = blockIdx.x / p.tiles_n, tn = blockIdx.x % p.tiles_n;
+  const long long tm = blockIdx.x / (uint32_t)p.tiles_n, tn = blockIdx.x % (uint32_t)p.tiles_n;
   const long long r0 = tm * kTile, c0 = tn * kTile;
   const long long np = p.tiles_n * kTile, mp = p.tiles_m * kTile;
   const MatrixScale g = matrix_scale<FMT>(p.gscale, b);
   const bool rows = p.codes != nullptr;
 
-  // 16 lanes a row, 16 rows a trip
-  const int cl = (lane & 15) * 8;
-#pragma unroll 4
-  for (int it = 0; it < kTile / 16; ++it) {
-    const int rl = it * 16 + warp * 2 + (lane >> 4);
-    const long long r = r0 + rl;
-    float x[8];
-    load8<DT>(row_ptr(p, b, r < p.m ? r : 0, kElem<DT>), c0 + cl, r < p.m ? p.n : 0, p.vec != 0, x);
-    if constexpr (DT == GM_F32) {
-      *reinterpret_cast<float4*>(tile + rl * kTile + cl) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4*>(tile + rl * kTile + cl + 4) = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-      uint32_t w[4];
+  // 16 lanes a row, 16 rows a trip; the loads of kAhead trips together
+  const int cl = (lane & 15) * 8, rl0 = warp * 2 + (lane >> 4);
+  constexpr int kAhead = DT == GM_F32 ? 4 : 8;
+#pragma unroll 1
+  for (int it0 = 0; it0 < kTile / 16; it0 += kAhead) {
+    Eight<DT> x[kAhead];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = (uint32_t)float_to_h16(x[2 * j], DT == GM_F16) |
-               ((uint32_t)float_to_h16(x[2 * j + 1], DT == GM_F16) << 16);
-      *reinterpret_cast<uint4*>(tile + rl * kTile + cl) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < kAhead; ++i) {
+      const long long r = r0 + (it0 + i) * 16 + rl0;
+      load8<DT>(row_ptr(p, b, r < p.m ? r : 0, kElem<DT>), c0 + cl, r < p.m ? p.n : 0, p.vec != 0, x[i]);
     }
-    if (rows) {
-      uint32_t top = top8(x);
 #pragma unroll
-      for (int o = 1; o < L; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      float mul;
-      const uint32_t s = block_scale<FMT>(__uint_as_float(top), g, mul);
-      const int j = cl / BL;
-      if (cl % BL == 0) sR[j / 4 * 512 + mx4_atom_byte(rl, j % 4)] = (uint8_t)(r < p.m ? s : 0u);
-      if (r < p.m)
-        *reinterpret_cast<uint32_t*>(p.codes + ((b * (long long)p.m + r) * np + c0 + cl) / 2) =
-            codes8<FMT>(x, s, mul, g);
+    for (int i = 0; i < kAhead; ++i) {
+      const int rl = (it0 + i) * 16 + rl0;
+      const long long r = r0 + rl;
+#pragma unroll
+      for (int q = 0; q < W / 4; ++q)
+        reinterpret_cast<uint4*>(tile + (rl * kTile + cl) / 8 * W)[q] =
+            make_uint4(x[i].w[4 * q], x[i].w[4 * q + 1], x[i].w[4 * q + 2], x[i].w[4 * q + 3]);
+      if (rows) {
+        uint32_t top = top8<DT>(x[i]);
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float mul;
+        const uint32_t s = block_scale<FMT>(__uint_as_float(top), g, mul);
+        const int j = cl / BL;
+        if (cl % BL == 0) sR[j / 4 * 512 + mx4_atom_byte(rl, j % 4)] = (uint8_t)(r < p.m ? s : 0u);
+        if (r < p.m) {
+          float v[8];
+          to_floats<DT>(x[i], v);
+          *reinterpret_cast<uint32_t*>(p.codes + ((b * (long long)p.m + r) * np + c0 + cl) / 2) =
+              codes8<FMT>(v, s, mul, g);
+        }
+      }
     }
   }
   __syncthreads();
 
-  // columns 2 lane + 64 (warp & 1), + 1; rows 32 (warp >> 1) .. + 31
+  // Two neighbouring columns cc, cc + 1 (one word of 16-bit elements) of 32 rows a thread.
   const int cc = (warp & 1) * 64 + lane * 2, rb = (warp >> 1) * 32;
+  uint32_t w[2][4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const long long c = c0 + cc + h;
-    uint32_t w[4];
+  for (int k = 0; k < 32 / BL; ++k) {
+    uint32_t v[BL][DT == GM_F32 ? 2 : 1], t[2] = {0u, 0u};
 #pragma unroll
-    for (int k = 0; k < 32 / BL; ++k) {
-      uint32_t top = 0;
-      float x[BL];
-#pragma unroll
-      for (int i = 0; i < BL; ++i) {
-        const T v = tile[(rb + k * BL + i) * kTile + cc + h];
-        if constexpr (DT == GM_F32) x[i] = v;
-        else x[i] = h16_to_float(v, DT == GM_F16);
-        top = max(top, __float_as_uint(fabsf(x[i])));
+    for (int i = 0; i < BL; ++i) {
+      const int at = (rb + k * BL + i) * kTile + cc;
+      if constexpr (DT == GM_F32) {
+        const uint2 u = *reinterpret_cast<const uint2*>(tile + at);
+        v[i][0] = u.x;
+        v[i][1] = u.y;
+        t[0] = max_magnitude<DT>(t[0], u.x);
+        t[1] = max_magnitude<DT>(t[1], u.y);
+      } else {
+        v[i][0] = tile[at / 2];
+        t[0] = max_magnitude<DT>(t[0], v[i][0]);
       }
+    }
+    if constexpr (DT != GM_F32) {
+      const uint32_t u = t[0];
+      t[0] = __float_as_uint(lo_half<DT>(u));
+      t[1] = __float_as_uint(hi_half<DT>(u));
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
       float mul;
-      const uint32_t s = block_scale<FMT>(__uint_as_float(top), g, mul);
+      const uint32_t s = block_scale<FMT>(__uint_as_float(t[h]), g, mul);
       const int j = rb / BL + k;
-      sC[j / 4 * 512 + mx4_atom_byte(cc + h, j % 4)] = (uint8_t)(c < p.n ? s : 0u);
+      sC[j / 4 * 512 + mx4_atom_byte(cc + h, j % 4)] = (uint8_t)(c0 + cc + h < p.n ? s : 0u);
 #pragma unroll
       for (int q = 0; q < BL / 8; ++q) {
         float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[q * 8 + e];
-        w[k * (BL / 8) + q] = codes8<FMT>(y, s, mul, g);
+        for (int e = 0; e < 8; ++e) {
+          if constexpr (DT == GM_F32) y[e] = __uint_as_float(v[q * 8 + e][h]);
+          else y[e] = h ? hi_half<DT>(v[q * 8 + e][0]) : lo_half<DT>(v[q * 8 + e][0]);
+        }
+        w[h][k * (BL / 8) + q] = codes8<FMT>(y, s, mul, g);
       }
     }
-    if (c < p.n)
-      *reinterpret_cast<uint4*>(p.codesT + ((b * (long long)p.n + c) * mp + r0 + rb) / 2) =
-          make_uint4(w[0], w[1], w[2], w[3]);
   }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (c0 + cc + h < p.n)
+      *reinterpret_cast<uint4*>(p.codesT + ((b * (long long)p.n + c0 + cc + h) * mp + r0 + rb) / 2) =
+          make_uint4(w[h][0], w[h][1], w[h][2], w[h][3]);
   __syncthreads();
   // atoms [row tile][along the row]: NA per tile
   for (int i = threadIdx.x; i < NA * 128; i += kThreads) {
@@ -397,7 +449,22 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequant(int m, int n, long lon
     const float v = __fmul_rn(e2m1_value(code), f);
     return FMT == GM_NV4 ? __fmul_rn(v, gs) : v;
   };
-  if (vec) {
+  if (vec == 8) {
+    // 32 bytes a lane (fp32 rows of a multiple of 8)
+#pragma unroll
+    for (int u = 0; u < kRowSpan / 256; ++u) {
+      const long long c = c0 + u * 256 + lane * 8;
+      if (c >= n) continue;
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(row + c / 2);
+      const float f = factor(c);
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = value(w >> (4 * e) & 15u, f);
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<float*>(out) + at + c),
+                   "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                   : "memory");
+    }
+  } else if (vec) {
     // neighbouring lanes write neighbouring groups of four (n is a multiple of 4)
 #pragma unroll
     for (int u = 0; u < kRowSpan / 128; ++u) {
@@ -475,7 +542,7 @@ cudaError_t launch_mx4_dequant(int B, int m, int n, int fmt, const uint8_t* code
                                const float* gscale, void* out, int odt, cudaStream_t s) {
   const long long spans = cdivll(n, kRowSpan), tiles_m = cdivll(m, kTile);
   const dim3 grid((unsigned)(cdivll(m, 8) * spans), B);
-  const int vec = n % 4 == 0;
+  const int vec = odt == GM_F32 && n % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 32 == 0 ? 8 : n % 4 == 0 ? 4 : 0;
   if (fmt == GM_MX4)
     k_mx4_dequant<GM_MX4><<<grid, kThreads, 0, s>>>(m, n, tiles_m, codes, scales, gscale, out, odt, vec, spans);
   else
