@@ -6,8 +6,8 @@
 // GM_NV4 (blocks of 16): gs = fp32(max|X| / 2688), sb = e4m3(max|x| / (6 gs)), codes
 //   e2m1(x / (sb gs)). 2688 = 6 * 448, so the largest block scale is e4m3's largest.
 //   Codes and scales are those of the exact quotients: fp32 decides unless the value
-//   lies so close to a border that fp32's error could cross it (about one in 10^5),
-//   then fp64 does (a border times sb gs has at most 31 bits: exact there).
+//   lies so close to a border that fp32's error could cross it, then the product of
+//   border and scales is compared with the value exactly.
 //
 // Both are bound by HBM: x once (2 or 4 B), 0.53 or 0.56 B per orientation; GM_NV4
 // reads x before that for the matrix scale.
@@ -129,7 +129,14 @@ __device__ __forceinline__ MatrixScale matrix_scale(const float* gscale, int b) 
   return g;
 }
 
-// e4m3 nearest to top / (6 gs), in fp64 (out of line: it runs for one block in 10^4).
+// |a| against border * gs, exactly, for gs well inside fp32's range: the border has at
+// most 7 bits; its product with gs is h + l with h rounded, l the exact rest, and an
+// fp32 a other than h lies on h's side of the sum. Does `a` round up (a tie: to even)?
+__device__ __forceinline__ bool rounds_up(float a, float border, float gs, bool even_is_up) {
+  const float h = border * gs, l = fmaf(border, gs, -h);
+  return a != h ? a > h : l != 0.f ? l < 0.f : even_is_up;
+}
+// e4m3 nearest to top / (6 gs), in fp64: for gs near either end of fp32.
 __device__ __noinline__ uint32_t exact_scale(float top, float gs) {
   // 3 fraction bits, exponents from -6, at most 448
   const double t = (double)top / (6.0 * (double)gs);
@@ -154,51 +161,45 @@ __device__ __forceinline__ uint32_t block_scale(float top, const MatrixScale& g,
   } else {
     mul = 0.f;
     if (!(g.gs > 0.f && g.gs <= 3.402823466e38f)) return 0u;   // a zero matrix, or one that is NaN
-    uint32_t b;
-    bool sure = !g.exact;
-    if (sure) {
-      const float t = top * g.inv6;
-      const uint32_t q = e4m3x2(t * kBelow, t * kAbove);
-      b = q & 255u;
-      sure = b == (q >> 8);
-    }
-    if (!sure) b = exact_scale(top, g.gs);
+    const float t = top * g.inv6;
+    const uint32_t q = e4m3x2(t * kBelow, t * kAbove);
+    uint32_t b = q & 255u;
+    if (b != q >> 8)
+      b += rounds_up(top, 3.f * (e4m3_value(b) + e4m3_value(b + 1)), g.gs, (b & 1) != 0) ? 1u : 0u;
+    if (g.exact) b = exact_scale(top, g.gs);
     // within 2^-22 of 1 / (sb gs); where it leaves fp32's range the codes are exact_codes'
     if (b) mul = __fdividef(1.0f, e4m3_value(b) * g.gs);
     return b;
   }
 }
 
-// Codes of eight elements under sb gs: |x| against border * sb * gs, a product of at
-// most 31 bits, exact in fp64.
+// Codes of eight elements of a GM_NV4 block in fp64, where sb gs times a border (31 bits
+// at most) is exact: for gs near either end of fp32.
 struct Values {
   float x[8];
 };
 __device__ __noinline__ uint32_t exact_codes(Values v, float sb, float gs) {
   const double s = (double)sb * (double)gs;
   uint32_t w = 0;
-#pragma unroll
+#pragma unroll 1
   for (int e = 0; e < 8; ++e) {
     const double a = fabs((double)v.x[e]);
-    uint32_t c = (a > 0.25 * s) + (a >= 0.75 * s) + (a > 1.25 * s) + (a >= 1.75 * s) + (a > 2.5 * s) +
-                 (a >= 3.5 * s) + (a > 5.0 * s);
-    if (v.x[e] < 0.f) c |= 8u;
-    w |= c << (4 * e);
+    const uint32_t c = (a > 0.25 * s) + (a >= 0.75 * s) + (a > 1.25 * s) + (a >= 1.75 * s) + (a > 2.5 * s) +
+                       (a >= 3.5 * s) + (a > 5.0 * s);
+    w |= (c | (v.x[e] < 0.f ? 8u : 0u)) << (4 * e);
   }
   return w;
 }
 
-// Codes of eight elements of one block.
-template <int FMT>
-__device__ __forceinline__ uint32_t codes8(const float (&x)[8], uint32_t b, float mul, const MatrixScale& g) {
+// Codes of eight elements of one block; at(e) reads element e again.
+template <int FMT, typename At>
+__device__ __forceinline__ uint32_t codes8(const float (&x)[8], uint32_t b, float mul, const MatrixScale& g, At&& at) {
   float y[8];
   if constexpr (FMT == GM_MX4) {
-    if (b == 255u) return 0u;
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = x[e] * mul;
-    return e2m1x8(y);
+    return b == 255u ? 0u : e2m1x8(y);
   } else {
-    if (b == 0u) return 0u;
     float z[8];
     const float below = mul * kBelow, above = mul * kAbove;
 #pragma unroll
@@ -206,9 +207,19 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8], uint32_t b, floa
       y[e] = x[e] * below;
       z[e] = x[e] * above;
     }
-    uint32_t w = e2m1x8(y);
-    if (w != e2m1x8(z) || g.exact)
-      w = exact_codes(Values{x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]}, e4m3_value(b), g.gs);
+    uint32_t w = e2m1x8(y), d = w ^ e2m1x8(z);
+    if (b == 0u) return 0u;
+    if (g.exact) return exact_codes(Values{x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]}, e4m3_value(b), g.gs);
+    // One call in fifty with bf16 inputs (gs = max|X| / 2688 puts the borders of some
+    // block scales on multiples of max|X|): one element at a time, read again, for an
+    // index that varies would move all of them to local memory.
+    while (d) {
+      const int i = (__ffs(d) - 1) & ~3;             // the element's nibble
+      d &= ~(15u << i);
+      const uint32_t c = w >> i & 7u;                // one step below the other; the border between:
+      const float border = __uint_as_float((2 * c + 1) << 21) * 8.507059173023462e37f;   // as e2m1_value
+      if (rounds_up(fabsf(at(i >> 2)), border * e4m3_value(b), g.gs, (c & 1) != 0)) w += 1u << i;
+    }
     return w;
   }
 }
@@ -297,7 +308,8 @@ __global__ void __launch_bounds__(kThreads) k_mx4_rows(const QuantParams p, long
     if (live && c < np) {
       float v[8];
       to_floats<DT>(x[u], v);
-      *reinterpret_cast<uint32_t*>(p.codes + ((b * (long long)p.m + r) * np + c) / 2) = codes8<FMT>(v, s, mul, g);
+      *reinterpret_cast<uint32_t*>(p.codes + ((b * (long long)p.m + r) * np + c) / 2) =
+          codes8<FMT>(v, s, mul, g, [&](int e) { return load_as_float(row, c + e, DT); });
     }
     // lane 4 L i gathers the bytes of lanes 4 L i, + L, + 2 L, + 3 L
     uint32_t w = s;
@@ -329,6 +341,10 @@ __global__ void __launch_bounds__(kThreads) k_mx4_tile(const QuantParams p) {
 
   // 16 lanes a row, 16 rows a trip; the loads of kAhead trips together
   const int cl = (lane & 15) * 8, rl0 = warp * 2 + (lane >> 4);
+  auto element = [&](int r, int c) {   // of the tile
+    if constexpr (DT == GM_F32) return __uint_as_float(tile[r * kTile + c]);
+    else return h16_to_float(reinterpret_cast<const uint16_t*>(tile)[r * kTile + c], DT == GM_F16);
+  };
   constexpr int kAhead = DT == GM_F32 ? 4 : 8;
 #pragma unroll 1
   for (int it0 = 0; it0 < kTile / 16; it0 += kAhead) {
@@ -358,7 +374,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_tile(const QuantParams p) {
           float v[8];
           to_floats<DT>(x[i], v);
           *reinterpret_cast<uint32_t*>(p.codes + ((b * (long long)p.m + r) * np + c0 + cl) / 2) =
-              codes8<FMT>(v, s, mul, g);
+              codes8<FMT>(v, s, mul, g, [&](int e) { return element(rl, cl + e); });
         }
       }
     }
@@ -404,7 +420,8 @@ __global__ void __launch_bounds__(kThreads) k_mx4_tile(const QuantParams p) {
           if constexpr (DT == GM_F32) y[e] = __uint_as_float(v[q * 8 + e][h]);
           else y[e] = h ? hi_half<DT>(v[q * 8 + e][0]) : lo_half<DT>(v[q * 8 + e][0]);
         }
-        w[h][k * (BL / 8) + q] = codes8<FMT>(y, s, mul, g);
+        w[h][k * (BL / 8) + q] =
+            codes8<FMT>(y, s, mul, g, [&](int e) { return element(rb + k * BL + q * 8 + e, cc + h); });
       }
     }
   }
