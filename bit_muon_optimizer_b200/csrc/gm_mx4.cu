@@ -33,9 +33,9 @@ struct Eight {
 };
 // From column c of a row of n (zeros behind its end).
 template <int DT>
-__device__ __forceinline__ void load8(const void* row, long long c, long long n, bool vec, Eight<DT>& x) {
+__device__ __forceinline__ void load8(const void* row, int c, int n, bool vec, Eight<DT>& x) {
   if (vec && c + 8 <= n) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + c * (DT == GM_F32 ? 4 : 2));
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + (size_t)c * (DT == GM_F32 ? 4 : 2));
     const uint4 a = p[0];
     x.w[0] = a.x; x.w[1] = a.y; x.w[2] = a.z; x.w[3] = a.w;
     if constexpr (DT == GM_F32) {
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_top(const QuantParams p) {
     long long r;
     if (items < (1LL << 31)) r = (uint32_t)i / (uint32_t)spans;   // a 64-bit division costs more than the loads
     else r = i / spans;
-    const long long c0 = (i - r * spans) * kRowSpan;
+    const int c0 = (int)(i - r * spans) * kRowSpan;
     const void* row = row_ptr(p, b, r, kElem<DT>);
     Eight<DT> x[kRowSpan / 256];
 #pragma unroll
@@ -284,22 +284,24 @@ __global__ void __launch_bounds__(kThreads) k_mx4_top(const QuantParams p) {
 template <int DT, int FMT>
 __global__ void __launch_bounds__(kThreads) k_mx4_rows(const QuantParams p, long long spans) {
   const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const long long r = blockIdx.x / spans * 8 + (threadIdx.x >> 5);
-  const long long c0 = blockIdx.x % spans * kRowSpan;
-  const long long np = mx4_padded(p.n), atoms = mx4_atoms(p.n, FMT);
+  const long long r = blockIdx.x / (uint32_t)spans * 8 + (threadIdx.x >> 5);
+  const int c0 = (int)(blockIdx.x % (uint32_t)spans) * kRowSpan;
+  const int np = (int)mx4_padded(p.n);
+  const long long atoms = mx4_atoms(p.n, FMT);
   constexpr int L = mx4_block(FMT) / 8;     // lanes of a block
   uint8_t* sc = p.scales + ((b * p.tiles_m + r / 128) * atoms) * 512 + mx4_atom_byte((int)(r % 128), 0);
   const bool live = r < p.m;
   const MatrixScale g = matrix_scale<FMT>(p.gscale, b);
   const void* row = row_ptr(p, b, live ? r : 0, kElem<DT>);
-  const long long n = live ? p.n : 0;
+  const int n = live ? p.n : 0;
+  uint8_t* codes = p.codes + (b * (long long)p.m + r) * (np / 2);
   Eight<DT> x[kRowSpan / 256];
 #pragma unroll
   for (int u = 0; u < kRowSpan / 256; ++u)
     load8<DT>(row, c0 + u * 256 + lane * 8, n, p.vec != 0, x[u]);
 #pragma unroll
   for (int u = 0; u < kRowSpan / 256; ++u) {
-    const long long c = c0 + u * 256 + lane * 8;
+    const int c = c0 + u * 256 + lane * 8;
     uint32_t top = top8(x[u]);
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_rows(const QuantParams p, long
     if (live && c < np) {
       float v[8];
       to_floats<DT>(x[u], v);
-      *reinterpret_cast<uint32_t*>(p.codes + ((b * (long long)p.m + r) * np + c) / 2) =
+      *reinterpret_cast<uint32_t*>(codes + c / 2) =
           codes8<FMT>(v, s, mul, g, [&](int e) { return load_as_float(row, c + e, DT); });
     }
     // lane 4 L i gathers the bytes of lanes 4 L i, + L, + 2 L, + 3 L
@@ -346,18 +348,24 @@ __global__ void __launch_bounds__(kThreads) k_mx4_tile(const QuantParams p) {
     else return h16_to_float(reinterpret_cast<const uint16_t*>(tile)[r * kTile + c], DT == GM_F16);
   };
   constexpr int kAhead = DT == GM_F32 ? 4 : 8;
+  // what is left of the matrix in this tile, and this thread's first row: the loops
+  // below count in 32 bits
+  const int mrem = (int)min((long long)kTile, p.m - r0), nrem = (int)min((long long)kTile, p.n - c0);
+  const uint8_t* src = row_ptr(p, b, r0, kElem<DT>) + (c0 + (long long)rl0 * p.ldx) * kElem<DT>;
+  const long long src_step = 16 * p.ldx * kElem<DT>;
+  const uint32_t row_bytes = (uint32_t)(np / 2);
+  uint8_t* dst = p.codes + ((b * (long long)p.m + r0 + rl0) * np + c0 + cl) / 2;
 #pragma unroll 1
   for (int it0 = 0; it0 < kTile / 16; it0 += kAhead) {
     Eight<DT> x[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const long long r = r0 + (it0 + i) * 16 + rl0;
-      load8<DT>(row_ptr(p, b, r < p.m ? r : 0, kElem<DT>), c0 + cl, r < p.m ? p.n : 0, p.vec != 0, x[i]);
+      load8<DT>(src, cl, (it0 + i) * 16 + rl0 < mrem ? nrem : 0, p.vec != 0, x[i]);
+      src += src_step;
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int rl = (it0 + i) * 16 + rl0;
-      const long long r = r0 + rl;
 #pragma unroll
       for (int q = 0; q < W / 4; ++q)
         reinterpret_cast<uint4*>(tile + (rl * kTile + cl) / 8 * W)[q] =
@@ -369,13 +377,13 @@ __global__ void __launch_bounds__(kThreads) k_mx4_tile(const QuantParams p) {
         float mul;
         const uint32_t s = block_scale<FMT>(__uint_as_float(top), g, mul);
         const int j = cl / BL;
-        if (cl % BL == 0) sR[j / 4 * 512 + mx4_atom_byte(rl, j % 4)] = (uint8_t)(r < p.m ? s : 0u);
-        if (r < p.m) {
+        if (cl % BL == 0) sR[j / 4 * 512 + mx4_atom_byte(rl, j % 4)] = (uint8_t)(rl < mrem ? s : 0u);
+        if (rl < mrem) {
           float v[8];
           to_floats<DT>(x[i], v);
-          *reinterpret_cast<uint32_t*>(p.codes + ((b * (long long)p.m + r) * np + c0 + cl) / 2) =
-              codes8<FMT>(v, s, mul, g, [&](int e) { return element(rl, cl + e); });
+          *reinterpret_cast<uint32_t*>(dst) = codes8<FMT>(v, s, mul, g, [&](int e) { return element(rl, cl + e); });
         }
+        dst += 16 * (size_t)row_bytes;
       }
     }
   }
@@ -411,7 +419,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_tile(const QuantParams p) {
       float mul;
       const uint32_t s = block_scale<FMT>(__uint_as_float(t[h]), g, mul);
       const int j = rb / BL + k;
-      sC[j / 4 * 512 + mx4_atom_byte(cc + h, j % 4)] = (uint8_t)(c0 + cc + h < p.n ? s : 0u);
+      sC[j / 4 * 512 + mx4_atom_byte(cc + h, j % 4)] = (uint8_t)(cc + h < nrem ? s : 0u);
 #pragma unroll
       for (int q = 0; q < BL / 8; ++q) {
         float y[8];
@@ -427,7 +435,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_tile(const QuantParams p) {
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    if (c0 + cc + h < p.n)
+    if (cc + h < nrem)
       *reinterpret_cast<uint4*>(p.codesT + ((b * (long long)p.n + c0 + cc + h) * mp + r0 + rb) / 2) =
           make_uint4(w[h][0], w[h][1], w[h][2], w[h][3]);
   __syncthreads();
@@ -449,16 +457,16 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequant(int m, int n, long lon
                                                           const float* __restrict__ gscale, void* out,
                                                           int odt, int vec, long long spans) {
   const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const long long r = blockIdx.x / spans * 8 + (threadIdx.x >> 5);
+  const long long r = blockIdx.x / (uint32_t)spans * 8 + (threadIdx.x >> 5);
   if (r >= m) return;
-  const long long c0 = blockIdx.x % spans * kRowSpan;
+  const int c0 = (int)(blockIdx.x % (uint32_t)spans) * kRowSpan;
   const long long np = mx4_padded(n), atoms = mx4_atoms(n, FMT);
   const uint8_t* sc = scales + ((b * tiles_m + r / 128) * atoms) * 512 + mx4_atom_byte((int)(r % 128), 0);
   const float gs = FMT == GM_NV4 ? gscale[b] : 1.f;
   const uint8_t* row = codes + (b * (long long)m + r) * (np / 2);
   const long long at = (b * (long long)m + r) * n;
-  auto factor = [&](long long c) {
-    const long long j = c / mx4_block(FMT);
+  auto factor = [&](int c) {
+    const int j = c / mx4_block(FMT);
     const uint32_t sb = sc[j / 4 * 512 + j % 4];
     return FMT == GM_MX4 ? e8m0_value(sb) : e4m3_value(sb);
   };
@@ -470,7 +478,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequant(int m, int n, long lon
     // 32 bytes a lane (fp32 rows of a multiple of 8)
 #pragma unroll
     for (int u = 0; u < kRowSpan / 256; ++u) {
-      const long long c = c0 + u * 256 + lane * 8;
+      const int c = c0 + u * 256 + lane * 8;
       if (c >= n) continue;
       const uint32_t w = *reinterpret_cast<const uint32_t*>(row + c / 2);
       const float f = factor(c);
@@ -485,7 +493,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequant(int m, int n, long lon
     // neighbouring lanes write neighbouring groups of four (n is a multiple of 4)
 #pragma unroll
     for (int u = 0; u < kRowSpan / 128; ++u) {
-      const long long c = c0 + u * 128 + lane * 4;
+      const int c = c0 + u * 128 + lane * 4;
       if (c >= n) continue;
       const uint32_t w = *reinterpret_cast<const uint16_t*>(row + c / 2);
       const float f = factor(c);
@@ -496,7 +504,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequant(int m, int n, long lon
     // rows off alignment: neighbouring lanes write neighbouring elements
 #pragma unroll 8
     for (int u = 0; u < kRowSpan / 32; ++u) {
-      const long long c = c0 + u * 32 + lane;
+      const int c = c0 + u * 32 + lane;
       if (c >= n) break;
       store_from_float(out, at + c, odt, value((uint32_t)row[c / 2] >> (4 * (c & 1)) & 15u, factor(c)));
     }
