@@ -241,6 +241,13 @@ __device__ __forceinline__ const uint8_t* row_ptr(const QuantParams& p, int b, l
 template <int DT>
 constexpr int kElem = DT == GM_F32 ? 4 : 2;
 
+// The kernel that finds GM_NV4's matrix scale, the one that quantises and the product
+// that takes the codes are launched as programmatic dependents: the next may start (its
+// set-up, and loads that the one before does not write) once every CTA of the one before
+// has, and waits for its results where it needs them.
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------- the matrix scale
 // gscale[b] = max over elements of fp32(|x| / 2688) by atomicMax on its bits (the
 // order does not matter; division is monotone, so this is the quotient of the
@@ -248,6 +255,7 @@ constexpr int kElem = DT == GM_F32 ? 4 : 2;
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_mx4_top(const QuantParams p) {
   const int b = blockIdx.y, lane = threadIdx.x & 31;
+  next_may_start();
   uint32_t top = 0;
   // a warp takes pieces of 1024 elements of a row
   const long long spans = cdivll(p.n, kRowSpan), items = spans * p.m;
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_rows(const QuantParams p, long
   constexpr int L = mx4_block(FMT) / 8;     // lanes of a block
   uint8_t* sc = p.scales + ((b * p.tiles_m + r / 128) * atoms) * 512 + mx4_atom_byte((int)(r % 128), 0);
   const bool live = r < p.m;
-  const MatrixScale g = matrix_scale<FMT>(p.gscale, b);
+  next_may_start();
   const void* row = row_ptr(p, b, live ? r : 0, kElem<DT>);
   const int n = live ? p.n : 0;
   uint8_t* codes = p.codes + (b * (long long)p.m + r) * (np / 2);
@@ -299,6 +307,8 @@ __global__ void __launch_bounds__(kThreads) k_mx4_rows(const QuantParams p, long
 #pragma unroll
   for (int u = 0; u < kRowSpan / 256; ++u)
     load8<DT>(row, c0 + u * 256 + lane * 8, n, p.vec != 0, x[u]);
+  if constexpr (FMT == GM_NV4) wait_for_previous();
+  const MatrixScale g = matrix_scale<FMT>(p.gscale, b);
 #pragma unroll
   for (int u = 0; u < kRowSpan / 256; ++u) {
     const int c = c0 + u * 256 + lane * 8;
@@ -338,8 +348,9 @@ __global__ void __launch_bounds__(kThreads) k_mx4_tile(const QuantParams p) {
   const long long tm = blockIdx.x / (uint32_t)p.tiles_n, tn = blockIdx.x % (uint32_t)p.tiles_n;
   const long long r0 = tm * kTile, c0 = tn * kTile;
   const long long np = p.tiles_n * kTile, mp = p.tiles_m * kTile;
-  const MatrixScale g = matrix_scale<FMT>(p.gscale, b);
   const bool rows = p.codes != nullptr;
+  next_may_start();
+  MatrixScale g;
 
   // 16 lanes a row, 16 rows a trip; the loads of kAhead trips together
   const int cl = (lane & 15) * 8, rl0 = warp * 2 + (lane >> 4);
@@ -362,6 +373,10 @@ __global__ void __launch_bounds__(kThreads) k_mx4_tile(const QuantParams p) {
     for (int i = 0; i < kAhead; ++i) {
       load8<DT>(src, cl, (it0 + i) * 16 + rl0 < mrem ? nrem : 0, p.vec != 0, x[i]);
       src += src_step;
+    }
+    if (it0 == 0) {
+      if constexpr (FMT == GM_NV4) wait_for_previous();
+      g = matrix_scale<FMT>(p.gscale, b);
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
@@ -511,6 +526,22 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequant(int m, int n, long lon
   }
 }
 
+// `dependent`: after k_mx4_top, whose result the kernel waits for.
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, size_t smem, bool dependent, cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = pdl;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int DT, int FMT>
 cudaError_t quant_t(int B, const QuantParams& p, cudaStream_t s) {
   if constexpr (FMT == GM_NV4) {
@@ -530,12 +561,10 @@ cudaError_t quant_t(int B, const QuantParams& p, cudaStream_t s) {
       const cudaError_t e = smem_attr_once(once, k_mx4_tile<DT, FMT>, bytes);
       if (e != cudaSuccess) return e;
     }
-    k_mx4_tile<DT, FMT><<<dim3((unsigned)(p.tiles_m * p.tiles_n), B), kThreads, bytes, s>>>(p);
-  } else {
-    const long long spans = cdivll(mx4_padded(p.n), kRowSpan);
-    k_mx4_rows<DT, FMT><<<dim3((unsigned)(p.tiles_m * 16 * spans), B), kThreads, 0, s>>>(p, spans);
+    return launch(k_mx4_tile<DT, FMT>, dim3((unsigned)(p.tiles_m * p.tiles_n), B), bytes, FMT == GM_NV4, s, p);
   }
-  return cudaGetLastError();
+  const long long spans = cdivll(mx4_padded(p.n), kRowSpan);
+  return launch(k_mx4_rows<DT, FMT>, dim3((unsigned)(p.tiles_m * 16 * spans), B), 0, FMT == GM_NV4, s, p, spans);
 }
 
 }  // namespace

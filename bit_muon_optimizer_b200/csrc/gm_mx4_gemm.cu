@@ -354,6 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (group > 1) cluster_sync_all();   // barriers initialised before any signal from another CTA
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  // Launched as a programmatic dependent: the set-up above runs under the kernel before
+  // (often the quantisation of an operand), whose results are visible from here on.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // First row of this CTA's part of a tile in the instruction's first operand (CG = 2: A,
   // CG = 1: B) and in its second.
@@ -613,12 +616,14 @@ cudaError_t launch_t(const Maps& m, const ProductParams& p, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem_bytes(CG, FMT);
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)group;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k_mx4_gemm<CG, FMT>, m.A, m.B, m.SA, m.SB, p);
 }
 
