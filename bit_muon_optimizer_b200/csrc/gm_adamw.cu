@@ -121,8 +121,8 @@ constexpr float kScaleFloor = 1.17549435e-38f;   // 2^-126
 constexpr float kTopM = 448.0f, kTopR = 1.9375f;
 
 __device__ __forceinline__ float scale_of(float top, float inv_max) {
-  // a group with an infinity or a NaN is NaN as a whole
-  return top <= 3.402823466e38f ? fmaxf(__fmul_rn(top, inv_max), kScaleFloor) : __int_as_float(0x7fffffff);
+  // an infinity or a NaN stays: it decides what the whole group stands for
+  return top <= 3.402823466e38f ? fmaxf(__fmul_rn(top, inv_max), kScaleFloor) : top;
 }
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t d;
@@ -406,7 +406,13 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
     near |= gap <= 40u || wm.x != (e4m3x2(hi[0], hi[1]) | (e4m3x2(hi[2], hi[3]) << 16)) ||
             wm.y != (e4m3x2(hi[4], hi[5]) | (e4m3x2(hi[6], hi[7]) << 16));
     uint2 wv = make_uint2(bytes4(cr[0], cr[1], cr[2], cr[3]), bytes4(cr[4], cr[5], cr[6], cr[7]));
-    const bool finite = tm <= 3.402823466e38f && tv <= 3.402823466e38f;   // else the group is NaN
+    const bool finite = tm <= 3.402823466e38f && tv <= 3.402823466e38f;
+    if (!(tv <= 3.402823466e38f)) {
+      // codes 1 for what is not zero: infinite (or NaN) under this scale
+#pragma unroll
+      for (int e = 0; e < 8; ++e) cr[e] = min(vb[e], 1u);
+      wv = make_uint2(bytes4(cr[0], cr[1], cr[2], cr[3]), bytes4(cr[4], cr[5], cr[6], cr[7]));
+    }
     if (__any_sync(0xffffffffu, near)) {
       const Codes8 o = exact_codes(k, coef->c, Eight{g[0], g[1], g[2], g[3], g[4], g[5], g[6], g[7]}, mc, vc, ms, vs);
       if (finite) {

@@ -387,3 +387,42 @@ def test_offsets_beyond_32_bits(cuda_lib):
     assert torch.equal(p[-tail:], pt[0]) and torch.equal(st.m[0][-tail:], s2.m[0])
     assert torch.equal(st.v[0][-tail:], s2.v[0]) and torch.equal(st.mscale[0][-3:], s2.mscale[0])
     assert int(st.m[0][:-tail].count_nonzero()) == 0 and int(p[:-tail].count_nonzero()) == 0
+
+
+def test_nonfinite_moments_of_a_group(cuda_lib):
+    """What a group of 8-bit moments stands for once a NaN or an infinity is in it: m
+    NaN; v NaN or infinite (its zeros NaN); step after step, its neighbours as ever."""
+    gm = cuda_lib
+    for bad, want in ((math.nan, torch.isnan), (math.inf, torch.isposinf), (-math.inf, torch.isposinf)):
+        p, g = _inputs([400], F32, F32, 18)
+        g[0][200] = bad
+        pd, gd, st = [p[0].to(DEV)], [g[0].to(DEV)], _state(gm, [400], 8, 18, 5)
+        for _ in range(3):
+            gm.AdamWStep(**HP)(st, pd, gd)
+            m, v = st.moments()
+            torch.cuda.synchronize()
+            inside = torch.zeros(400, dtype=torch.bool, device=DEV)
+            inside[128:256] = True
+            assert torch.equal(torch.isnan(m[0]), inside) and torch.equal(want(v[0]), inside)
+            assert bool(torch.isfinite(v[0][~inside]).all())
+
+
+def test_states_follow_the_definition_for_many_steps(cuda_lib):
+    """Ten free-running steps with 8-bit states: codes and scales bit for bit the
+    oracle's, which runs in fp64 from its own state (scales kept in fp32)."""
+    gm = cuda_lib
+    n = 5000
+    b1, b2 = HP["betas"]
+    p, _ = _inputs([n], F32, BF16, 71)
+    pd, st = [p[0].to(DEV)], _state(gm, [n], 8, 71, 20)
+    ref = [x[0].cpu() for x in (st.m, st.mscale, st.v, st.vscale)]
+    for t in range(21, 31):
+        g = _inputs([n], F32, BF16, 100 + t)[1][0]
+        gm.AdamWStep(**HP)(st, pd, [g.to(DEV)])
+        _, m, v = OA.step(p[0], g, *OA.decode8(*ref), t, HP["lr"], b1, b2, HP["eps"], HP["wd"])
+        cm, sm, cv, sv = OA.encode8(m, v)
+        ref = [cm, sm.float(), cv, sv.float()]
+        torch.cuda.synchronize()
+        live = cm % 128 > 0
+        assert torch.equal(st.m[0].cpu()[live], cm[live]) and torch.equal(st.v[0].cpu(), cv), t
+        assert torch.equal(st.mscale[0].cpu(), ref[1]) and torch.equal(st.vscale[0].cpu(), ref[3]), t
