@@ -357,7 +357,12 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
       const float r0 = root_value((e < 4 ? vc.x : vc.y) >> (8 * (e & 3)) & 255u) * va, g0 = g[e] * cv;
       size[e] = fabsf(a) + fabsf(b);
       m[e] = a + b;
-      const float v = fmaf(r0, r0, g0 * g0);
+      float v = fmaf(r0, r0, g0 * g0);
+      if constexpr (!WHOLE) {
+        // behind the tensor's end: nothing, whatever the group's scales are (0 under an
+        // infinite scale would be a NaN)
+        if (e >= n) m[e] = size[e] = v = 0.f;
+      }
       // Approximations (2^-21 of an update) and factors taken out of the loop keep this
       // kernel off its issue rate. A v below 2^-126 has a root below 1.1e-19, taken as
       // zero: nothing beside an eps of 1e-15.
@@ -381,7 +386,7 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
     // then the groups are redone in fp64. Errors, u = 2^-24: m is off by 5 u size at
     // most (two products of three roundings, one sum), and m / sm by that, by 6 u, and
     // by sm's relative error, 5 u size / tm of the top element: size up to 3 tm is
-    // allowed for (26 u size in all), a group with more is redone. r is off by 16 u.
+    // allowed for (26 u size in all), a group with more is redone. r / sv is off by 23 u.
     // Near fp32's subnormals these bounds do not hold: 2^-90 and 2^-80 keep the
     // smallest element that gets a code (2^-18 of the top) and its square above them,
     // and 2^14 keeps 1 / sv 2^112 below.
@@ -396,14 +401,14 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
       const float y = m[e] * im;
       lo[e] = fmaf(size[e], -w, y);
       hi[e] = fmaf(size[e], w, y);
-      // a border is at a set bit 18 with zeros below; +-20 around it
-      const uint32_t bits = __float_as_uint(r[e] * iv) + 0x40000u + 20u;
+      // a border is at a set bit 18 with zeros below; +-24 (24 to 48 u) around it
+      const uint32_t bits = __float_as_uint(r[e] * iv) + 0x40000u + 24u;
       gap = min(gap, bits & 0x7FFFFu);
       cr[e] = max(bits >> 19, min(vb[e], 1u));
     }
     uint2 wm = make_uint2(e4m3x2(lo[0], lo[1]) | (e4m3x2(lo[2], lo[3]) << 16),
                           e4m3x2(lo[4], lo[5]) | (e4m3x2(lo[6], lo[7]) << 16));
-    near |= gap <= 40u || wm.x != (e4m3x2(hi[0], hi[1]) | (e4m3x2(hi[2], hi[3]) << 16)) ||
+    near |= gap <= 48u || wm.x != (e4m3x2(hi[0], hi[1]) | (e4m3x2(hi[2], hi[3]) << 16)) ||
             wm.y != (e4m3x2(hi[4], hi[5]) | (e4m3x2(hi[6], hi[7]) << 16));
     uint2 wv = make_uint2(bytes4(cr[0], cr[1], cr[2], cr[3]), bytes4(cr[4], cr[5], cr[6], cr[7]));
     const bool finite = tm <= 3.402823466e38f && tv <= 3.402823466e38f;

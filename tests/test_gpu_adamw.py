@@ -426,3 +426,20 @@ def test_states_follow_the_definition_for_many_steps(cuda_lib):
         live = cm % 128 > 0
         assert torch.equal(st.m[0].cpu()[live], cm[live]) and torch.equal(st.v[0].cpu(), cv), t
         assert torch.equal(st.mscale[0].cpu(), ref[1]) and torch.equal(st.vscale[0].cpu(), ref[3]), t
+
+
+@pytest.mark.parametrize("n", [1, 5, 130])
+def test_infinite_scale_of_a_ragged_group(cuda_lib, n):
+    """What lies behind a tensor's end stays out of its last group, also when that
+    group's scales are infinite: v infinite (not NaN) step after step."""
+    gm = cuda_lib
+    p, g = _inputs([n], F32, F32, 19)
+    g[0][-1] = math.inf
+    for t in (F32, BF16):
+        pd, gd, st = [p[0].to(DEV)], [g[0].to(t).to(DEV)], _state(gm, [n], 8, 19, 5)
+        for _ in range(3):
+            gm.AdamWStep(**HP)(st, pd, gd)
+            _, v = st.moments()
+            torch.cuda.synchronize()
+            last = torch.arange(n, device=DEV) // 128 == (n - 1) // 128
+            assert torch.equal(torch.isposinf(v[0]), last)
