@@ -516,12 +516,25 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequant(int m, int n, long lon
                                                       value(w >> 8 & 15u, f), value(w >> 12, f)));
     }
   } else {
-    // rows off alignment: neighbouring lanes write neighbouring elements
-#pragma unroll 8
-    for (int u = 0; u < kRowSpan / 32; ++u) {
-      const int c = c0 + u * 32 + lane;
+    // rows off alignment: eight elements a lane, turned in shared memory so that
+    // neighbouring lanes write neighbouring elements
+    __shared__ float turn[kThreads / 32][256];
+    float* t = turn[threadIdx.x >> 5];
+#pragma unroll 1
+    for (int u = 0; u < kRowSpan / 256; ++u) {
+      const int c = c0 + u * 256;
       if (c >= n) break;
-      store_from_float(out, at + c, odt, value((uint32_t)row[c / 2] >> (4 * (c & 1)) & 15u, factor(c)));
+      if (c + lane * 8 < n) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(row + c / 2 + lane * 4);
+        const float f = factor(c + lane * 8);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[lane * 8 + e] = value(w >> (4 * e) & 15u, f);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e * 32 + lane < n) store_from_float(out, at + c + e * 32 + lane, odt, t[e * 32 + lane]);
+      __syncwarp();
     }
   }
 }
