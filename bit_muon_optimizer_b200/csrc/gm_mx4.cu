@@ -9,8 +9,13 @@
 //   lies so close to a border that fp32's error could cross it, then the product of
 //   border and scales is compared with the value exactly.
 //
-// Both are bound by HBM: x once (2 or 4 B), 0.53 or 0.56 B per orientation; GM_NV4
-// reads x before that for the matrix scale.
+// HBM moves x once (2 or 4 B) and 0.53 or 0.56 B per orientation; GM_NV4 reads x before
+// that for the matrix scale. What bounds the kernels is issue: 8192 x 8192 bf16 both
+// ways take 18 instructions an element (GM_MX4, 54 us, 3.8 TB/s) or 33 (GM_NV4, 92 us:
+// twice the products and conversions, for each element is coded a little below and a
+// little above its quotient to see whether fp32 decides). 16384 x 8192 bf16, GM_MX4:
+// rows 65 us (5.2 TB/s), both 96 us; 18944 x 3584 fp32, GM_NV4, both: 150 us with its
+// matrix scale (6.0 TB/s for that pass).
 
 #include <math.h>
 

@@ -6,18 +6,26 @@
 // One kernel, two shapes:
 //   CG = 2: a pair of CTAs per 256 x 256 tile (M = 256, N = 256, K = 64 per
 //     instruction), persistent over the tiles. Each CTA loads its 128 rows of A and
-//     128 of the 256 rows of B: per flop the fewest bytes from L2, which bounds the
-//     large products.
+//     128 of the 256 rows of B. 8192 x 18944 x 3584 into bf16: 237 us (GM_MX4, 4.7
+//     PFLOP/s), 230 us (GM_NV4) at 1.6 GHz under the power cap; without its stores 174 us,
+//     with a quarter of its MMAs 196 us, with neither 124 us (36 KB a stage and SM, 68
+//     bytes a clock, is what L2 delivers). So loads, MMAs and stores share the memory
+//     path of an SM: 64 bytes a clock of copies into shared memory, as many of operand
+//     reads at the tensor pipe's full rate, and D's lines going out. Stores through
+//     shared memory (250 us) or of whole lines exchanged among lanes (242 us), a fifth
+//     stage, other orders of the tiles and scales fetched a stage ahead gained nothing.
 //   CG = 1, for products of few tiles, which B's bytes (a weight's) bound: operands
 //     change places, so that a tile is 128 rows of B (the instruction's M) by up to 256
 //     rows of A (its N, no more than there are, to 16). One CTA per tile, or a cluster of
 //     up to 8 that split K stage by stage and join their fp32 parts through distributed
 //     shared memory in the order of the ranks (so equal operands give equal bits). A lane
-//     holds a column of D, and its stores are contiguous for any N.
+//     holds a column of D, and its stores are contiguous for any N. 1 x 3584 x 18944: 13.6
+//     us, of which 7 us stream the weight's 36 MB at 5.7 TB/s, 3.3 us pass before the first
+//     byte arrives and 2.5 us after the last (join, cluster barriers).
 // Roles of a CTA's warps:
 //   warp 0: TMA of A's codes and scales      warp 2: TMA of B's
-//   warp 1: tensor memory; one thread copies a stage's scales to tensor memory
-//           (tcgen05.cp) and issues its MMAs
+//   warp 1: tensor memory; copies a stage's scales to tensor memory (tcgen05.cp) and
+//           issues its MMAs, one lane issuing under a predicate
 //   warps 4..19: epilogue. A warp takes 32 rows and 64 columns into registers at
 //           once, so that the accumulator is free for the next tile before the
 //           results are written.
@@ -641,6 +649,9 @@ cudaError_t launch_mx4_matmul(int B, int M, int N, int K, int fmt, const uint8_t
   p.ag = ag; p.bg = bg;
   p.err = device_error_word();
   if (!p.err) return cudaErrorUnknown;
+  // Pairs from a quarter of the SMs' worth of tiles on (2048 x 2048 x 2048: 64 tiles, 11.7
+  // us); up to 128 rows a tile of one CTA reads the weight as fast (16 x 18944 x 3584: 12.6
+  // us, 15.5 as pairs), and few tiles leave pairs idle (1001 x 2053 x 771: 8.7 us alone).
   const bool pair = M > 128 && (long long)cdiv(M, 256) * cdiv(N, kBN) * B >= sm_count() / 4;
   p.split = 1;
   Maps m;
@@ -660,7 +671,8 @@ cudaError_t launch_mx4_matmul(int B, int M, int N, int K, int fmt, const uint8_t
     const long long tiles = (long long)p.tiles_m * p.tiles_n * B;
     const int nst = cdiv((int)(mx4_padded(K) / 64), kStageK / 64);
     // A join costs about 2 us and a quarter of a stage's time per eight rows; a split
-    // halves the stages.
+    // halves the stages (1001 x 2053 x 771, four stages: 15.9 us split in two, 8.7 whole;
+    // 1 x 3584 x 18944, 74 stages: 13.6 us split in four).
     while (p.split < kMaxSplit && tiles * p.split * 2 <= sm_count() && nst >= (8 + p.bn / 8) * p.split) p.split *= 2;
     ok = map_codes(&m.A, b, B, N, K, 128) && map_codes(&m.B, a, B, M, K, p.bn) &&
          map_scales(&m.SA, bs, B, N, K, fmt, 1) && map_scales(&m.SB, as, B, M, K, fmt, p.sf_tiles);
