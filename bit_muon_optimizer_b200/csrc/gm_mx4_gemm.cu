@@ -7,7 +7,7 @@
 //   CG = 2: a pair of CTAs per 256 x 256 tile (M = 256, N = 256, K = 64 per
 //     instruction), persistent over the tiles. Each CTA loads its 128 rows of A and
 //     128 of the 256 rows of B. 8192 x 18944 x 3584 into bf16: 237 us (GM_MX4, 4.7
-//     PFLOP/s), 230 us (GM_NV4) at 1.6 GHz under the power cap; without its stores 174 us,
+//     PFLOP/s), 230 us (GM_NV4) at 1.6 GHz; without its stores 174 us,
 //     with a quarter of its MMAs 196 us, with neither 124 us (36 KB a stage and SM, 68
 //     bytes a clock, is what L2 delivers). So loads, MMAs and stores share the memory
 //     path of an SM: 64 bytes a clock of copies into shared memory, as many of operand
@@ -20,8 +20,8 @@
 //     up to 8 that split K stage by stage and join their fp32 parts through distributed
 //     shared memory in the order of the ranks (so equal operands give equal bits). A lane
 //     holds a column of D, and its stores are contiguous for any N. 1 x 3584 x 18944: 13.6
-//     us, of which 7 us stream the weight's 36 MB at 5.7 TB/s, 3.3 us pass before the first
-//     byte arrives and 2.5 us after the last (join, cluster barriers).
+//     us. In a cold launch with timers in it (14.9 us) the first stage is there after 4.1
+//     us, the last 8 us later (36 MB, 4.5 TB/s); the join and its barriers end 2.8 us on.
 // Roles of a CTA's warps:
 //   warp 0: TMA of A's codes and scales      warp 2: TMA of B's
 //   warp 1: tensor memory; copies a stage's scales to tensor memory (tcgen05.cp) and
