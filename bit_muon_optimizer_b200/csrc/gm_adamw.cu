@@ -434,14 +434,15 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
     } else {
       // The scales are rounded from fp64 too: a last place of fp32 in a scale would move
       // the next step's codes. The first lane that holds the group's top element computes
-      // that element again.
+      // the first such element again (in a group of zeros element 0, the only one that
+      // lies inside every tensor's last group).
       const int first = lane & 16;
       const uint32_t om = __ballot_sync(0xffffffffu, tmb == gm) >> first & 0xFFFFu;
       const uint32_t ov = __ballot_sync(0xffffffffu, tvb == gv) >> first & 0xFFFFu;
       if (in && lane - first == __ffs(om) - 1) {
         int e = 0;
 #pragma unroll
-        for (int j = 7; j > 0; --j) e = __float_as_uint(fabsf(m[j])) == gm ? j : e;
+        for (int j = 7; j >= 0; --j) e = __float_as_uint(fabsf(m[j])) == gm ? j : e;
         const double md = (double)e4m3_value((e < 4 ? mc.x : mc.y) >> (8 * (e & 3)) & 255u) * (double)ms;
         const double gd = __dmul_rn((double)one<GDT>(E.g, i + e), coef->c);
         const double d = fabs(__dadd_rn(__dmul_rn(k.db1, md), __dmul_rn(k.dob1, gd)));
@@ -450,7 +451,7 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
       if (in && lane - first == __ffs(ov) - 1) {
         int e = 0;
 #pragma unroll
-        for (int j = 7; j > 0; --j) e = vb[j] == gv ? j : e;
+        for (int j = 7; j >= 0; --j) e = vb[j] == gv ? j : e;
         const double rd = (double)root_value((e < 4 ? vc.x : vc.y) >> (8 * (e & 3)) & 255u) * (double)vs;
         const double gd = __dmul_rn((double)one<GDT>(E.g, i + e), coef->c);
         const double d = __dadd_rn(__dmul_rn(k.db2, __dmul_rn(rd, rd)), __dmul_rn(k.dob2, __dmul_rn(gd, gd)));

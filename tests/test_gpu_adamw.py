@@ -443,3 +443,23 @@ def test_infinite_scale_of_a_ragged_group(cuda_lib, n):
             torch.cuda.synchronize()
             last = torch.arange(n, device=DEV) // 128 == (n - 1) // 128
             assert torch.equal(torch.isposinf(v[0]), last)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("n", [1, 129, 257])
+def test_zero_group_of_one_element(cuda_lib, n, dt):
+    """A last group of one element that is zero, moments too: its scales are the
+    smallest ones, whatever lies behind the gradient's end (here NaN)."""
+    gm = cuda_lib
+    buf = torch.full((n + 8,), math.nan, dtype=dt, device=DEV)
+    g = buf[:n]
+    g.copy_(WL.random_matrix((n,), 3, std=1e-3))
+    g[n - 1] = 0
+    p = torch.ones(n, device=DEV)
+    st = gm.AdamWState.zeros([p], 8)
+    for _ in range(2):
+        gm.AdamWStep(**HP)(st, [p], [g])
+    torch.cuda.synchronize()
+    assert float(st.mscale[0][-1]) == float(st.vscale[0][-1]) == 2.0 ** -126
+    assert int(st.m[0][-1]) == int(st.v[0][-1]) == 0
+    assert bool(torch.isfinite(p).all()) and bool(torch.isfinite(st.mscale[0]).all())
