@@ -368,7 +368,7 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
       }
       // Approximations (2^-21 of an update) and factors taken out of the loop keep this
       // kernel off its issue rate. A v below 2^-126 has a root below 1.1e-19, taken as
-      // zero: nothing beside an eps of 1e-15.
+      // zero: nothing beside an eps of 1e-12, the least that is accepted.
       r[e] = approx_sqrt(v);
       p[e] = fmaf(p[e], f.decay, -m[e] * approx_rcp(fmaf(r[e], f.root8, f.eps8)));
       vb[e] = __float_as_uint(v);     // never negative: ordered like the values, a NaN above

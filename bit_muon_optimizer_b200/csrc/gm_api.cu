@@ -763,7 +763,8 @@ static gm_status adamw_params_check(const gm_adamw_params* p) {
   GM_CHECK_ARG(std::isfinite(p->lr) && std::isfinite(p->wd), "lr and wd must be finite");
   GM_CHECK_ARG(p->beta1 >= 0.0 && p->beta1 < 1.0 && p->beta2 >= 0.0 && p->beta2 < 1.0,
                "beta1 and beta2 lie in [0, 1)");
-  GM_CHECK_ARG(std::isfinite(p->eps) && p->eps >= 1e-30, "eps must be finite and at least 1e-30");
+  GM_CHECK_ARG(std::isfinite(p->eps) && p->eps >= (p->bits == 8 ? 1e-12 : 1e-30),
+               "eps must be finite and at least 1e-30 (1e-12 with 8-bit states)");
   GM_CHECK_ARG(aligned(p->clip, 8) && aligned(p->lr_dev, 4), "misaligned clip or lr_dev");
   return GM_OK;
 }

@@ -420,7 +420,8 @@ gm_status gm_grad_norm(int count, const gm_grad* grads, double max_norm, float* 
  * in fp32, p rounded once to its dtype.
  *   tensors: host array of `count` entries (1 <= count <= 65536; may be reused once
  *   the call returns) of device arrays of numel >= 1 elements, element alignment
- *   sufficing (arrays that are not 16-byte aligned move element by element):
+ *   sufficing (a tensor with an array that is not aligned to eight of its elements
+ *   moves element by element):
  *     p [numel] of pdt, in place; g [numel] of gdt; copy (nullable): the new p
  *     rounded to cdt (a 16-bit working copy);
  *     params->bits = 32: m, v f32 [numel];
@@ -446,7 +447,7 @@ gm_status gm_grad_norm(int count, const gm_grad* grads, double max_norm, float* 
  */
 #define GM_ADAMW_SCRATCH_BYTES 64
 typedef struct {
-  double lr, beta1, beta2, eps, wd;
+  double lr, beta1, beta2, eps, wd;   /* eps >= 1e-30, with 8-bit states 1e-12 */
   int bits;                  /* states: 32 or 8 */
   const double* clip;        /* device [1], nullable: factor of the gradients */
   const float* lr_dev;       /* device [1], nullable: takes lr's place (a schedule under

@@ -151,3 +151,15 @@ def test_zero_states_have_their_layout():
         assert all(bool((t == 0).all()) for t in st.tensors())
         c = st.clone()
         assert c.bits == st.bits and c.m[0].data_ptr() != st.m[0].data_ptr()
+
+
+@pytest.mark.parametrize("bits,least", [(32, 1e-30), (8, 1e-12)])
+def test_least_eps(bits, least):
+    """An eps beside which the 8-bit step's root, zero for a v below 2^-126, would
+    matter is refused."""
+    table = np.array([[4096] * 6 + [0, 8]], dtype=np.int64)
+    for eps in (least * 0.99, 0.0, -1.0, math.nan):
+        prm = gm.AdamWParams(1e-3, 0.9, 0.999, eps, 0.0, bits, None, None)
+        assert gm.lib.gm_adamw_step(1, table.ctypes.data, 0, 0, 0, ctypes.byref(prm), 4096, None, 4096,
+                                    None) == gm.GM_E_ARG
+        assert b"eps" in gm.lib.gm_last_error()
