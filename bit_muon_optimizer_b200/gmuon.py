@@ -953,6 +953,11 @@ class AdamWStep:
                    _addresses(copies) if copies is not None else none, numels]
         if len(set(columns[0])) != n or len(set(columns[2])) != n:
             raise ValueError("params: a tensor is in the list more than once")
+        kept = [a for column in columns[2:6 if state.bits == 8 else 4] for a in column]
+        if len(set(kept)) != len(kept):
+            raise ValueError("state: a tensor is in the state more than once")
+        if copies is not None and len(set(columns[6])) != n:
+            raise ValueError("copies: a tensor is in the list more than once")
         prm = AdamWParams(self.lr if lr is None else float(lr), *self.betas, self.eps, self.wd,
                           state.bits, clip.scale.data_ptr() if clip is not None else None, lr_dev)
         flag = skip.data_ptr() if skip is not None else None

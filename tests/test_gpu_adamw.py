@@ -463,3 +463,78 @@ def test_zero_group_of_one_element(cuda_lib, n, dt):
     assert float(st.mscale[0][-1]) == float(st.vscale[0][-1]) == 2.0 ** -126
     assert int(st.m[0][-1]) == int(st.v[0][-1]) == 0
     assert bool(torch.isfinite(p).all()) and bool(torch.isfinite(st.mscale[0]).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_tensor_written_twice_is_refused(cuda_lib, bits):
+    gm = cuda_lib
+    p, g = [torch.ones(300, device=DEV) for _ in range(2)], [torch.ones(300, device=DEV)] * 2
+    step = gm.AdamWStep(**HP)
+    names = ["m", "v"] + (["mscale", "vscale"] if bits == 8 else [])
+    for name in names:
+        st = gm.AdamWState.zeros(p, bits)
+        getattr(st, name)[1] = getattr(st, name)[0]
+        with pytest.raises(ValueError, match="more than once"):
+            step(st, p, g)
+    st = gm.AdamWState.zeros(p, bits)
+    st.v = st.m
+    with pytest.raises(ValueError, match="more than once"):
+        step(st, p, g)
+    st = gm.AdamWState.zeros(p, bits)
+    with pytest.raises(ValueError, match="copies"):
+        step(st, p, g, copies=[torch.empty(300, device=DEV, dtype=BF16)] * 2)
+    step(st, p, g, copies=p)                      # an fp32 copy may be the parameter itself
+    torch.cuda.synchronize()
+    assert int(st.step) == 1 and all(bool(torch.isfinite(x).all()) for x in p)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("lr", [0.0, -1e-3])
+def test_rates_of_zero_and_below(cuda_lib, bits, lr):
+    """A rate of zero leaves the parameters bit for bit as they were and moves the
+    states; a negative one is the formula's."""
+    gm = cuda_lib
+    sizes = [1, 129, 5000]
+    p, g = _inputs(sizes, F32, F32, 4)
+    pd, gd = [x.to(DEV) for x in p], [x.to(DEV) for x in g]
+    st = _state(gm, sizes, bits, 4, 7)
+    before = [_old(st, i) for i in range(3)]
+    gm.AdamWStep(**{**HP, "lr": lr})(st, pd, gd)
+    torch.cuda.synchronize()
+    for i in range(3):
+        if lr == 0.0:
+            assert torch.equal(pd[i].cpu(), p[i])
+        want, m, v = OA.step(p[i], g[i], *before[i], 8, lr, *HP["betas"], HP["eps"], HP["wd"])
+        # as in the module's bounds, with |lr|
+        b1, b2 = HP["betas"]
+        S = b1 * before[i][0].abs() + (1 - b1) * g[i].double().abs()
+        den = (v / (1 - b2 ** 8)).sqrt() + HP["eps"]
+        tol = 3 * U * p[i].double().abs() + abs(lr) / (1 - b1 ** 8) * (5 * U * S + 12 * U * m.abs()) / den
+        assert bool(((pd[i].double().cpu() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_two_streams_step_two_states(cuda_lib, bits):
+    """Steps of different states at the same time, one with a norm into a kept
+    result, give the bits of steps one after the other."""
+    gm = cuda_lib
+    sizes = [70001, 129, 1]
+    step = gm.AdamWStep(**HP)
+
+    def start(seed):
+        p, g = _inputs(sizes, F32, BF16, seed)
+        return [x.to(DEV) for x in p], [x.to(DEV) for x in g], _state(gm, sizes, bits, seed, 3)
+    ends = []
+    for together in (False, True):
+        work = [start(s) for s in (11, 12)]
+        norms = [gm.grad_norm(g * 40, 1e-3) for _, g, _ in work]       # longer lists than the ones below
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in work]
+        for _ in range(3):
+            for (p, g, st), s, nrm in zip(work, streams, norms):
+                with torch.cuda.stream(s if together else torch.cuda.current_stream()):
+                    step(st, p, g, clip=gm.grad_norm(g, 1e-3, out=nrm))
+        torch.cuda.synchronize()
+        ends.append([t.clone() for p, _, st in work for t in (*p, *st.tensors())])
+    for a, b in zip(*ends):
+        assert torch.equal(a.view(torch.uint8) if a.dtype == F32 else a, b.view(torch.uint8) if b.dtype == F32 else b)
