@@ -414,3 +414,31 @@ def test_linear_layers_step_ends_in_the_optimizers(cuda_lib, fmt):
     short = 1e-8 / (float(res.scale) * gbias.double().abs() + 1e-8)
     assert bool((move.abs() <= 1e-2 * (short + 16 * U)).all())
     _check(gm, gm.mx4_quant(W, f), W.cpu(), fmt)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 40, 300), (1, 300, 4100), (2048, 1500, 200)])
+@pytest.mark.parametrize("ga,gb", [(1e20, 1e19), (3e30, 2e8), (1e-20, 1e-20), (1e-30, 1e-13), (1e25, 1e-25)])
+def test_matrix_scales_whose_product_leaves_fp32(cuda_lib, M, N, K, ga, gb):
+    """GM_NV4: the product of both gscale overflows, is subnormal, or is ordinary,
+    while the sums times it lie in fp32's range. Entries are small beside the one that
+    makes gscale, which meets zeros. An entry of D near fp32's end may be off by its
+    last step, 2^-149; the exponent's halves multiply exactly otherwise."""
+    gm = cuda_lib
+    size = 0.02 if ga * gb > 1e30 else 300.0
+
+    def operand(r, seed, gs, at, other):
+        x = WL.random_matrix((1, r, K), seed).double().clamp(-4, 4) * size
+        x[:, :, other] = 0
+        x[:, :, at] = 0
+        x[0, 0, at] = 2688.0
+        x[0, -1] *= 1.0 if r == 1 else 0.0            # a row of zeros
+        return gm.mx4_quant((x * gs).float().to(DEV), gm.GM_NV4)
+    A, Bm = operand(M, 1, ga, 3, 40), operand(N, 2, gb, 40, 3)
+    a, b = _values(gm, A).to(DEV), _values(gm, Bm).to(DEV)
+    want, S = a @ b.transpose(-1, -2), a.abs() @ b.abs().transpose(-1, -2)
+    assert float(want.abs().max()) < 1.6e38
+    D = gm.mx4_matmul(A, Bm, out_dtype=F32)
+    tol = (math.ceil(K / 64) + 2) * 2.0 ** -22 * S + U * want.abs() + 2.0 ** -149
+    assert bool(((D.double() - want).abs() <= tol).all())
+    gm.mx4_matmul(A, Bm, out=D, accumulate=True)
+    assert bool(((D.double() - 2 * want).abs() <= 2 * tol + 2 * U * want.abs()).all())
