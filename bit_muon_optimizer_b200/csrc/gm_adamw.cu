@@ -434,15 +434,16 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
     } else {
       // The scales are rounded from fp64 too: a last place of fp32 in a scale would move
       // the next step's codes. The first lane that holds the group's top element computes
-      // the first such element again (in a group of zeros element 0, the only one that
-      // lies inside every tensor's last group).
+      // such an element again. (A top of zero is the padding's too; of a ragged group's
+      // first lane only element 0 is sure to lie inside the tensor.)
       const int first = lane & 16;
       const uint32_t om = __ballot_sync(0xffffffffu, tmb == gm) >> first & 0xFFFFu;
       const uint32_t ov = __ballot_sync(0xffffffffu, tvb == gv) >> first & 0xFFFFu;
       if (in && lane - first == __ffs(om) - 1) {
         int e = 0;
 #pragma unroll
-        for (int j = 7; j >= 0; --j) e = __float_as_uint(fabsf(m[j])) == gm ? j : e;
+        for (int j = 7; j > 0; --j) e = __float_as_uint(fabsf(m[j])) == gm ? j : e;
+        if (!WHOLE && gm == 0u) e = 0;
         const double md = (double)e4m3_value((e < 4 ? mc.x : mc.y) >> (8 * (e & 3)) & 255u) * (double)ms;
         const double gd = __dmul_rn((double)one<GDT>(E.g, i + e), coef->c);
         const double d = fabs(__dadd_rn(__dmul_rn(k.db1, md), __dmul_rn(k.dob1, gd)));
@@ -451,7 +452,8 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
       if (in && lane - first == __ffs(ov) - 1) {
         int e = 0;
 #pragma unroll
-        for (int j = 7; j >= 0; --j) e = vb[j] == gv ? j : e;
+        for (int j = 7; j > 0; --j) e = vb[j] == gv ? j : e;
+        if (!WHOLE && gv == 0u) e = 0;
         const double rd = (double)root_value((e < 4 ? vc.x : vc.y) >> (8 * (e & 3)) & 255u) * (double)vs;
         const double gd = __dmul_rn((double)one<GDT>(E.g, i + e), coef->c);
         const double d = __dadd_rn(__dmul_rn(k.db2, __dmul_rn(rd, rd)), __dmul_rn(k.dob2, __dmul_rn(gd, gd)));
