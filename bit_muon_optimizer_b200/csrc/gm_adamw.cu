@@ -470,7 +470,9 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
 
 template <int PDT, int GDT, int BITS, int N>
 __global__ void __launch_bounds__(kThreads, 3) k_adamw(const __grid_constant__ Table<N> t, const Consts k,
-                                                       const Coef* __restrict__ coef) {
+                                                       const Coef* coef) {
+  // k_adamw_begin may still be writing *coef until here: no __restrict__, which would
+  // promise that nothing writes it while this kernel lives
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Coef f = *coef;
   if (f.skip) return;
@@ -627,9 +629,10 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(const __grid_constant__ 
 }
 
 // The partial sums in a fixed order, so that equal gradients give equal bits.
-__global__ void __launch_bounds__(kThreads) k_grad_norm_join(int n, const double* __restrict__ part,
-                                                             double max_norm, float* norm,
-                                                             double* scale, int32_t* status) {
+__global__ void __launch_bounds__(kThreads) k_grad_norm_join(int n, const double* part, double max_norm,
+                                                             float* norm, double* scale,
+                                                             int32_t* status) {
+  // (no __restrict__: part is written until the wait ends)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   double acc = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) acc += part[i];
