@@ -414,8 +414,9 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
     near |= gap <= 48u || wm.x != (e4m3x2(hi[0], hi[1]) | (e4m3x2(hi[2], hi[3]) << 16)) ||
             wm.y != (e4m3x2(hi[4], hi[5]) | (e4m3x2(hi[6], hi[7]) << 16));
     uint2 wv = make_uint2(bytes4(cr[0], cr[1], cr[2], cr[3]), bytes4(cr[4], cr[5], cr[6], cr[7]));
-    const bool finite = tm <= 3.402823466e38f && tv <= 3.402823466e38f;
-    if (!(tv <= 3.402823466e38f)) {
+    // each moment by itself: a v that passes fp32's range leaves m as it is defined
+    const bool finite_m = tm <= 3.402823466e38f, finite_v = tv <= 3.402823466e38f;
+    if (!finite_v) {
       // codes 1 for what is not zero: infinite (or NaN) under this scale
 #pragma unroll
       for (int e = 0; e < 8; ++e) cr[e] = min(vb[e], 1u);
@@ -423,13 +424,11 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
     }
     if (__any_sync(0xffffffffu, near)) {
       const Codes8 o = exact_codes(k, coef->c, Eight{g[0], g[1], g[2], g[3], g[4], g[5], g[6], g[7]}, mc, vc, ms, vs);
-      if (finite) {
-        wm = o.m;
-        wv = o.v;
-      }
+      if (finite_m) wm = o.m;
+      if (finite_v) wv = o.v;
       if ((lane & 15) == 0 && in) {
-        E.mscale[grp] = finite ? o.sm : sm;
-        E.vscale[grp] = finite ? o.sv : sv;
+        E.mscale[grp] = finite_m ? o.sm : sm;
+        E.vscale[grp] = finite_v ? o.sv : sv;
       }
     } else {
       // The scales are rounded from fp64 too: a last place of fp32 in a scale would move
@@ -447,7 +446,7 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
         const double md = (double)e4m3_value((e < 4 ? mc.x : mc.y) >> (8 * (e & 3)) & 255u) * (double)ms;
         const double gd = __dmul_rn((double)one<GDT>(E.g, i + e), coef->c);
         const double d = fabs(__dadd_rn(__dmul_rn(k.db1, md), __dmul_rn(k.dob1, gd)));
-        E.mscale[grp] = finite ? (float)fmax(__dmul_rn(d, 1.0 / 448.0), pow2d(-126)) : sm;
+        E.mscale[grp] = finite_m ? (float)fmax(__dmul_rn(d, 1.0 / 448.0), pow2d(-126)) : sm;
       }
       if (in && lane - first == __ffs(ov) - 1) {
         int e = 0;
@@ -460,7 +459,7 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
         // the root by one step of Newton's from fp32's: 2^-44
         const float r0 = approx_sqrt(tv), h = 0.5f * approx_rcp(fmaxf(r0, kScaleFloor));
         const double r1 = fma(fma(-(double)r0, (double)r0, d), (double)h, (double)r0);
-        E.vscale[grp] = finite ? (float)fmax(__dmul_rn(r1, 1.0 / 1.9375), pow2d(-126)) : sv;
+        E.vscale[grp] = finite_v ? (float)fmax(__dmul_rn(r1, 1.0 / 1.9375), pow2d(-126)) : sv;
       }
     }
     store8_codes<WHOLE>(static_cast<uint8_t*>(E.m), i, n, wm);

@@ -436,8 +436,9 @@ gm_status gm_grad_norm(int count, const gm_grad* grads, double max_norm, float* 
  *     are the nearest ones (ties to even) to m / sm and sqrt(v) / sv in fp64, each
  *     operation above rounded singly (/ 448 and / 1.9375 as products with the
  *     rounded reciprocal). A NaN that enters a group makes its m and v NaN as a
- *     whole; an infinity (or a g^2 past fp32's range, for v) leaves an infinite
- *     scale, under which m is NaN and v infinite.
+ *     whole; an infinity (for v: a sum past fp32's range) leaves an infinite scale,
+ *     under which m is NaN and v infinite. Each moment by itself: a v past fp32's
+ *     range leaves an m that is not as defined above.
  *     No two entries may overlap. All-zero codes and scales are the zero state.
  *   step int64 [1] (device): completed steps, incremented by this one; scratch:
  *   GM_ADAMW_SCRATCH_BYTES of device memory, 16-byte aligned, that belong to this
