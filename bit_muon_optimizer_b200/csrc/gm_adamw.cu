@@ -432,34 +432,48 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
       }
     } else {
       // The scales are rounded from fp64 too: a last place of fp32 in a scale would move
-      // the next step's codes. The first lane that holds the group's top element computes
-      // such an element again. (A top of zero is the padding's too; of a ragged group's
-      // first lane only element 0 is sure to lie inside the tensor.)
+      // the next step's codes. The group's fp64 maximum is in a lane whose fp32 maximum
+      // comes within kTie places of the group's: of two elements each m is off by 15 u of
+      // the top (5 u size, see above), each v by 10 u of itself (its factors, counted
+      // twice by the squares, and two roundings), and a place is u or more. The eight
+      // elements of such a lane are computed again, one a lane, m by the first eight lanes
+      // of the group's sixteen and v by the others; nearly always there is one such lane.
+      constexpr uint32_t kTie = 32;
       const int first = lane & 16;
-      const uint32_t om = __ballot_sync(0xffffffffu, tmb == gm) >> first & 0xFFFFu;
-      const uint32_t ov = __ballot_sync(0xffffffffu, tvb == gv) >> first & 0xFFFFu;
-      if (in && lane - first == __ffs(om) - 1) {
-        int e = 0;
+      const uint32_t om = __ballot_sync(0xffffffffu, gm ? tmb + kTie >= gm : lane == first);
+      const uint32_t ov = __ballot_sync(0xffffffffu, gv ? tvb + kTie >= gv : lane == first);
+      const bool of_v = (lane & 8) != 0;
+      const uint8_t* codes = static_cast<const uint8_t*>(of_v ? E.v : E.m);
+      const double scale = (double)(of_v ? vs : ms);
+      uint32_t todo = (of_v ? ov : om) >> first & 0xFFFFu;
+      const long long group0 = i - (lane & 15) * 8 + (lane & 7);
+      double d = 0.0;
+      do {
+        const long long at = group0 + (__ffs(todo) - 1) * 8;
+        if (todo && (WHOLE || at < E.numel)) {
+          const uint32_t code = codes[at];
+          double x = (double)(of_v ? root_value(code) : e4m3_value(code)) * scale;
+          double y = __dmul_rn((double)one<GDT>(E.g, at), coef->c);
+          if (of_v) {
+            x = __dmul_rn(x, x);
+            y = __dmul_rn(y, y);
+          }
+          d = fmax(d, fabs(__dadd_rn(__dmul_rn(of_v ? k.db2 : k.db1, x), __dmul_rn(of_v ? k.dob2 : k.dob1, y))));
+        }
+        todo &= todo - 1;
+      } while (__any_sync(0xffffffffu, todo));
 #pragma unroll
-        for (int j = 7; j > 0; --j) e = __float_as_uint(fabsf(m[j])) == gm ? j : e;
-        if (!WHOLE && gm == 0u) e = 0;
-        const double md = (double)e4m3_value((e < 4 ? mc.x : mc.y) >> (8 * (e & 3)) & 255u) * (double)ms;
-        const double gd = __dmul_rn((double)one<GDT>(E.g, i + e), coef->c);
-        const double d = fabs(__dadd_rn(__dmul_rn(k.db1, md), __dmul_rn(k.dob1, gd)));
-        E.mscale[grp] = finite_m ? (float)fmax(__dmul_rn(d, 1.0 / 448.0), pow2d(-126)) : sm;
+      for (int o = 4; o; o >>= 1) d = fmax(d, __shfl_xor_sync(0xffffffffu, d, o));
+      if (of_v) {
+        // the root by two of Newton's steps from fp32's (2^-21, 2^-42, fp64's last place)
+        const double r0 = (double)approx_sqrt(tv), h = (double)(0.5f * approx_rcp(fmaxf((float)r0, kScaleFloor)));
+        const double r1 = fma(fma(-r0, r0, d), h, r0);
+        d = fma(fma(-r1, r1, d), h, r1);
       }
-      if (in && lane - first == __ffs(ov) - 1) {
-        int e = 0;
-#pragma unroll
-        for (int j = 7; j > 0; --j) e = vb[j] == gv ? j : e;
-        if (!WHOLE && gv == 0u) e = 0;
-        const double rd = (double)root_value((e < 4 ? vc.x : vc.y) >> (8 * (e & 3)) & 255u) * (double)vs;
-        const double gd = __dmul_rn((double)one<GDT>(E.g, i + e), coef->c);
-        const double d = __dadd_rn(__dmul_rn(k.db2, __dmul_rn(rd, rd)), __dmul_rn(k.dob2, __dmul_rn(gd, gd)));
-        // the root by one step of Newton's from fp32's: 2^-44
-        const float r0 = approx_sqrt(tv), h = 0.5f * approx_rcp(fmaxf(r0, kScaleFloor));
-        const double r1 = fma(fma(-(double)r0, (double)r0, d), (double)h, (double)r0);
-        E.vscale[grp] = finite_v ? (float)fmax(__dmul_rn(r1, 1.0 / 1.9375), pow2d(-126)) : sv;
+      if (in && (lane & 7) == 0) {
+        const float f = (float)fmax(__dmul_rn(d, of_v ? 1.0 / 1.9375 : 1.0 / 448.0), pow2d(-126));
+        if (of_v) E.vscale[grp] = finite_v ? f : sv;
+        else E.mscale[grp] = finite_m ? f : sm;
       }
     }
     store8_codes<WHOLE>(static_cast<uint8_t*>(E.m), i, n, wm);
