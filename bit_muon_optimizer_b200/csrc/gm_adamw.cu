@@ -200,12 +200,13 @@ __device__ __forceinline__ uint32_t group_max(uint32_t x) {
 // What every chunk of a step needs, computed once per step by k_adamw_begin.
 struct Coef {
   double c;          // clip factor (1 without)
-  float c32;
+  float c1, c2;      // c = c1 c2 in fp32, c2 = 1 unless c is no normal fp32 number
   float decay;       // 1 - lr wd
   float scale;       // lr / (1 - b1^t)
   float root;        // 1 / sqrt(1 - b2^t)
   float root8, eps8; // root / scale, eps / scale: the update is m / (r root8 + eps8)
   int skip;
+  int wide;          // c times 1 - b1 or the root of 1 - b2 is no normal fp32 number
 };
 static_assert(sizeof(Coef) <= GM_ADAMW_SCRATCH_BYTES, "the step's scratch holds the coefficients");
 
@@ -221,7 +222,12 @@ __global__ void k_adamw_begin(double lr, double b1, double b2, double eps, doubl
   const double l = lr_dev ? (double)*lr_dev : lr;
   const double c = clip ? *clip : 1.0;
   out->c = c;
-  out->c32 = (float)c;
+  // What fp32 cannot hold of c: a power of two first, which is exact where it matters.
+  const bool low = fabs(c) < pow2d(-126), high = fabs(c) > pow2d(127);
+  const double c1 = low ? pow2d(-126) : high ? pow2d(126) : c;
+  out->c1 = (float)c1;
+  out->c2 = low || high ? (float)fmin(fmax(c / c1, -3e38), 3e38) : 1.f;
+  out->wide = high || (c != 0.0 && !(fabs(c) * fmin(1.0 - b1, sqrt(1.0 - b2)) >= pow2d(-126)));
   out->decay = (float)(1.0 - l * wd);
   const double s = l / (1.0 - pow(b1, (double)t)), r = 1.0 / sqrt(1.0 - pow(b2, (double)t));
   out->scale = (float)s;
@@ -310,8 +316,10 @@ __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, u
 }
 
 // Eight elements a lane, element i the first. WHOLE: the warp's part lies inside the
-// tensor, whose arrays are aligned to eight elements.
-template <int PDT, int GDT, int BITS, bool WHOLE>
+// tensor, whose arrays are aligned to eight elements. WIDE (8 bits): for clip factors that
+// fp32 cannot hold (a norm near fp32's end gives them): gradients times the factor in
+// fp64, and all codes from fp64.
+template <int PDT, int GDT, int BITS, bool WHOLE, bool WIDE>
 __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const Coef* coef, const Coef& f,
                                           long long i, int lane) {
   const long long n = E.numel - i;
@@ -324,7 +332,7 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
     load8<GM_F32, WHOLE>(E.v, i, n, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float gc = g[e] * f.c32;
+      const float gc = g[e] * f.c1 * f.c2;
       m[e] = fmaf(k.b1, m[e], k.ob1 * gc);
       v[e] = fmaf(k.b2, v[e], gc * gc * k.ob2);
       const float u = __fdiv_rn(m[e], fmaf(__fsqrt_rn(v[e]), f.root, k.eps));
@@ -342,7 +350,8 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
     const float ms = in ? E.mscale[grp] : 0.f, vs = in ? E.vscale[grp] : 0.f;
     // b1 sm and the roots of b2 and 1 - b2 go into the group's factors:
     // m' = code (b1 sm) + g (1 - b1) c, v' = (root sv sqrt(b2))^2 + (g c sqrt(1 - b2))^2
-    const float ma = k.b1 * ms, va = k.rb2 * vs, cm = k.ob1 * f.c32, cv = k.rob2 * f.c32;
+    const float ma = k.b1 * ms, va = k.rb2 * vs;
+    const float cm = WIDE ? k.ob1 : k.ob1 * f.c1, cv = WIDE ? k.rob2 : k.rob2 * f.c1;
     float m[8], size[8], r[8];
     uint32_t vb[8];
     {
@@ -356,8 +365,9 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
     uint32_t tvb = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float a = m[e] * ma, b = g[e] * cm;
-      const float r0 = root_value((e < 4 ? vc.x : vc.y) >> (8 * (e & 3)) & 255u) * va, g0 = g[e] * cv;
+      const float gc = WIDE ? (float)((double)g[e] * f.c) : g[e];
+      const float a = m[e] * ma, b = gc * cm;
+      const float r0 = root_value((e < 4 ? vc.x : vc.y) >> (8 * (e & 3)) & 255u) * va, g0 = gc * cv;
       size[e] = fabsf(a) + fabsf(b);
       m[e] = a + b;
       float v = fmaf(r0, r0, g0 * g0);
@@ -393,7 +403,7 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
     // Near fp32's subnormals these bounds do not hold: 2^-90 and 2^-80 keep the
     // smallest element that gets a code (2^-18 of the top) and its square above them,
     // and 2^14 keeps 1 / sv 2^112 below.
-    bool near = ts > 3.f * tm;
+    bool near = WIDE || ts > 3.f * tm;
     if (tm < 8.1e-28f || tv < 8.3e-25f || sv > 16384.f) near |= ts > 0.f || tvb > 0;
     const float im = approx_rcp(sm), iv = approx_rcp(sv) * 1.925929944387236e-34f;   // 2^-112
     const float w = im * 1.66893005e-6f;   // 28 u
@@ -481,25 +491,42 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
   }
 }
 
-template <int PDT, int GDT, int BITS, int N>
-__global__ void __launch_bounds__(kThreads, 3) k_adamw(const __grid_constant__ Table<N> t, const Consts k,
-                                                       const Coef* coef) {
-  // k_adamw_begin may still be writing *coef until here: no __restrict__, which would
-  // promise that nothing writes it while this kernel lives
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Coef f = *coef;
-  if (f.skip) return;
+template <int PDT, int GDT, int BITS, bool WIDE, int N>
+__device__ __forceinline__ void walk(const Table<N>& t, const Consts& k, const Coef* coef, const Coef& f) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int ti = 0;
   for (int chunk = blockIdx.x; chunk < t.map.total(); chunk += gridDim.x) {
     ti = t.map.find(chunk, ti);
     const Entry& E = t.e[ti];
     const long long base = (long long)(chunk - t.map.first[ti]) * kChunk + warp * kPart;
-    if (t.vec[ti] && base + kPart <= E.numel)
-      step_part<PDT, GDT, BITS, true>(E, k, coef, f, base + lane * 8, lane);
+    if (!WIDE && t.vec[ti] && base + kPart <= E.numel)
+      step_part<PDT, GDT, BITS, true, WIDE>(E, k, coef, f, base + lane * 8, lane);
     else if (base < E.numel)
-      step_part<PDT, GDT, BITS, false>(E, k, coef, f, base + lane * 8, lane);
+      step_part<PDT, GDT, BITS, false, WIDE>(E, k, coef, f, base + lane * 8, lane);
   }
+}
+// Out of line: no ordinary step comes here.
+template <int PDT, int GDT, int N>
+__device__ __noinline__ void walk_wide8(const Table<N>& t, const Consts k, const Coef* coef) {
+  const Coef f = *coef;
+  walk<PDT, GDT, 8, true>(t, k, coef, f);
+}
+
+template <int PDT, int GDT, int BITS, int N>
+__global__ void __launch_bounds__(kThreads, 3)
+    k_adamw(const __grid_constant__ Table<N> t, const Consts k, const Coef* coef) {
+  // k_adamw_begin may still be writing *coef until here: no __restrict__, which would
+  // promise that nothing writes it while this kernel lives
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Coef f = *coef;
+  if (f.skip) return;
+  if constexpr (BITS == 8) {
+    if (f.wide) {
+      walk_wide8<PDT, GDT>(t, k, coef);
+      return;
+    }
+  }
+  walk<PDT, GDT, BITS, false>(t, k, coef, f);
 }
 
 // ------------------------------------------------------ 8-bit states to fp32
