@@ -334,7 +334,8 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
     for (int e = 0; e < 8; ++e) {
       const float gc = g[e] * f.c1 * f.c2;
       m[e] = fmaf(k.b1, m[e], k.ob1 * gc);
-      v[e] = fmaf(k.b2, v[e], gc * gc * k.ob2);
+      // in this order: g^2 alone leaves fp32's range before (1 - b2) g^2 does
+      v[e] = fmaf(k.ob2 * gc, gc, k.b2 * v[e]);
       const float u = __fdiv_rn(m[e], fmaf(__fsqrt_rn(v[e]), f.root, k.eps));
       p[e] = fmaf(p[e], f.decay, -u * f.scale);
     }

@@ -763,8 +763,12 @@ static gm_status adamw_params_check(const gm_adamw_params* p) {
   GM_CHECK_ARG(std::isfinite(p->lr) && std::isfinite(p->wd), "lr and wd must be finite");
   GM_CHECK_ARG(p->beta1 >= 0.0 && p->beta1 < 1.0 && p->beta2 >= 0.0 && p->beta2 < 1.0,
                "beta1 and beta2 lie in [0, 1)");
-  GM_CHECK_ARG(std::isfinite(p->eps) && p->eps >= (p->bits == 8 ? 1e-12 : 1e-30),
-               "eps must be finite and at least 1e-30 (1e-12 with 8-bit states)");
+  // What a root of v loses below fp32's numbers (2^-75, with 8-bit states 2^-63), divided
+  // by sqrt(1 - beta2) at the first step, must stay small beside eps.
+  GM_CHECK_ARG(std::isfinite(p->eps) && p->eps >= (p->bits == 8 ? 1e-12 : 1e-18) &&
+                   p->eps * std::sqrt(1.0 - p->beta2) >= (p->bits == 8 ? 1e-16 : 1e-20),
+               "eps must be finite and at least 1e-18 (1e-12 with 8-bit states), and times "
+               "sqrt(1 - beta2) at least 1e-20 (1e-16)");
   GM_CHECK_ARG(aligned(p->clip, 8) && aligned(p->lr_dev, 4), "misaligned clip or lr_dev");
   return GM_OK;
 }

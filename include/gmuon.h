@@ -448,7 +448,9 @@ gm_status gm_grad_norm(int count, const gm_grad* grads, double max_norm, float* 
  */
 #define GM_ADAMW_SCRATCH_BYTES 64
 typedef struct {
-  double lr, beta1, beta2, eps, wd;   /* eps >= 1e-30, with 8-bit states 1e-12 */
+  /* eps >= 1e-18 (8-bit states: 1e-12) and eps sqrt(1 - beta2) >= 1e-20 (1e-16): a v
+     that fp32 loses below its numbers then moves an update by less than 1e-4 lr */
+  double lr, beta1, beta2, eps, wd;
   int bits;                  /* states: 32 or 8 */
   const double* clip;        /* device [1], nullable: factor of the gradients */
   const float* lr_dev;       /* device [1], nullable: takes lr's place (a schedule under
