@@ -4,6 +4,8 @@
 #include <stdarg.h>
 #include <atomic>
 #include <cmath>
+#include <memory>
+#include <new>
 #include <stdio.h>
 #include <string.h>
 
@@ -773,22 +775,27 @@ static gm_status adamw_params_check(const gm_adamw_params* p) {
   return GM_OK;
 }
 
+static gm_status adamw_tensor_check(int i, const gm_adamw_tensor& x, const gm_adamw_dtypes& dt, int bits) {
+  GM_CHECK_ARG(dtype_ok(dt.p) && dtype_ok(dt.g) && dtype_ok(dt.copy), "bad dtype");
+  GM_CHECK_ARG(x.p && x.g && x.m && x.v && x.numel >= 1, "NULL or empty array of tensor %d", i);
+  GM_CHECK_ARG(aligned(x.p, dtype_bytes(dt.p)) && aligned(x.g, dtype_bytes(dt.g)) &&
+                   aligned(x.copy, dtype_bytes(dt.copy)),
+               "an array of tensor %d is not aligned to its elements", i);
+  if (bits == 32)
+    GM_CHECK_ARG(aligned(x.m, 4) && aligned(x.v, 4), "a state of tensor %d is not aligned", i);
+  else
+    GM_CHECK_ARG(x.mscale && x.vscale && aligned(x.mscale, 4) && aligned(x.vscale, 4),
+                 "NULL or misaligned scales of tensor %d", i);
+  return GM_OK;
+}
+
 static gm_status adamw_list_check(int count, const gm_adamw_tensor* t, gm_dtype pdt, gm_dtype gdt,
                                   gm_dtype cdt, int bits) {
   GM_CHECK_ARG(count >= 1 && count <= kMaxList, "count=%d out of [1, %d]", count, kMaxList);
   GM_CHECK_ARG(t, "NULL list");
-  GM_CHECK_ARG(dtype_ok(pdt) && dtype_ok(gdt) && dtype_ok(cdt), "bad dtype");
   for (int i = 0; i < count; ++i) {
-    const gm_adamw_tensor& x = t[i];
-    GM_CHECK_ARG(x.p && x.g && x.m && x.v && x.numel >= 1, "NULL or empty array of tensor %d", i);
-    GM_CHECK_ARG(aligned(x.p, dtype_bytes(pdt)) && aligned(x.g, dtype_bytes(gdt)) &&
-                     aligned(x.copy, dtype_bytes(cdt)),
-                 "an array of tensor %d is not aligned to its elements", i);
-    if (bits == 32)
-      GM_CHECK_ARG(aligned(x.m, 4) && aligned(x.v, 4), "a state of tensor %d is not aligned", i);
-    else
-      GM_CHECK_ARG(x.mscale && x.vscale && aligned(x.mscale, 4) && aligned(x.vscale, 4),
-                   "NULL or misaligned scales of tensor %d", i);
+    const gm_status chk = adamw_tensor_check(i, t[i], {pdt, gdt, cdt}, bits);
+    if (chk != GM_OK) return chk;
   }
   return GM_OK;
 }
@@ -828,6 +835,37 @@ gm_status gm_adamw_step(int count, const gm_adamw_tensor* tensors, gm_dtype pdt,
   chk = gm_adamw_begin(params, step, skip, scratch, stream);
   if (chk != GM_OK) return chk;
   return gm_adamw_apply(count, tensors, pdt, gdt, cdt, params, scratch, stream);
+}
+
+gm_status gm_adamw_step_mixed(int count, const gm_adamw_tensor* tensors, const gm_adamw_dtypes* dtypes,
+                              const gm_adamw_params* params, int64_t* step, const int32_t* skip,
+                              void* scratch, gm_stream_t stream) {
+  gm_status chk = adamw_params_check(params);
+  if (chk != GM_OK) return chk;
+  GM_CHECK_ARG(count >= 1 && count <= 27 * kMaxList, "count=%d out of [1, %d]", count, 27 * kMaxList);
+  GM_CHECK_ARG(tensors && dtypes, "NULL list");
+  for (int i = 0; i < count; ++i) {   // every list before anything is enqueued
+    chk = adamw_tensor_check(i, tensors[i], dtypes[i], params->bits);
+    if (chk != GM_OK) return chk;
+  }
+  // the tensors of each combination of types together, in their order
+  const std::unique_ptr<gm_adamw_tensor[]> list(new (std::nothrow) gm_adamw_tensor[count]);
+  if (!list) return set_error(GM_E_WORKSPACE, "no host memory for a list of %d tensors", count);
+  int first[28] = {0}, at[27];
+  for (int i = 0; i < count; ++i) ++first[dtypes[i].p * 9 + dtypes[i].g * 3 + dtypes[i].copy + 1];
+  for (int k = 0; k < 27; ++k) {
+    GM_CHECK_ARG(first[k + 1] <= kMaxList, "%d tensors of one combination of types, at most %d", first[k + 1],
+                 kMaxList);
+    at[k] = first[k + 1] += first[k];
+  }
+  for (int i = count - 1; i >= 0; --i) list[--at[dtypes[i].p * 9 + dtypes[i].g * 3 + dtypes[i].copy]] = tensors[i];
+  chk = gm_adamw_begin(params, step, skip, scratch, stream);
+  if (chk != GM_OK) return chk;
+  for (int k = 0; k < 27; ++k)
+    if (first[k + 1] > first[k])
+      GM_CUDA(launch_adamw(first[k + 1] - first[k], list.get() + first[k], k / 9, k / 3 % 3, k % 3, *params,
+                           scratch, reinterpret_cast<cudaStream_t>(stream)));
+  return GM_OK;
 }
 
 gm_status gm_adamw_unpack8(int count, const gm_adamw_state8* tensors, gm_stream_t stream) {

@@ -124,6 +124,7 @@ ADAMW_SCRATCH_BYTES = 64
 _sig("gm_grad_norm_workspace_bytes", c_size_t, [c_int])
 _sig("gm_grad_norm", c_int, [c_int, vp, ctypes.c_double, vp, vp, vp, vp, c_size_t, vp])
 _sig("gm_adamw_step", c_int, [c_int, vp, c_int, c_int, c_int, ctypes.POINTER(AdamWParams), vp, vp, vp, vp])
+_sig("gm_adamw_step_mixed", c_int, [c_int, vp, vp, ctypes.POINTER(AdamWParams), vp, vp, vp, vp])
 _sig("gm_adamw_begin", c_int, [ctypes.POINTER(AdamWParams), vp, vp, vp, vp])
 _sig("gm_adamw_apply", c_int, [c_int, vp, c_int, c_int, c_int, ctypes.POINTER(AdamWParams), vp, vp])
 _sig("gm_mx4_codes_bytes", c_size_t, [c_int, c_int, c_int])
@@ -961,25 +962,18 @@ class AdamWStep:
         prm = AdamWParams(self.lr if lr is None else float(lr), *self.betas, self.eps, self.wd,
                           state.bits, clip.scale.data_ptr() if clip is not None else None, lr_dev)
         flag = skip.data_ptr() if skip is not None else None
+        table = _rows(*columns)
         with _on(dev):
             s = _stream_of(dev)
             if len(pk) == len(gk) == len(ck) == 1:
-                table = _rows(*columns)
                 _check(lib.gm_adamw_step(n, table, *[_DT[next(iter(k))] for k in (pk, gk, ck)],
                                          ctypes.byref(prm), state.step.data_ptr(), flag,
                                          state.scratch.data_ptr(), s), "gm_adamw_step")
-                return
-            kinds = {}
-            for i, row in enumerate(zip(*columns)):
-                kind = (_DT[params[i].dtype], _DT[grads[i].dtype],
-                        _DT[copies[i].dtype] if copies is not None else GM_F32)
-                kinds.setdefault(kind, []).append(row)
-            _check(lib.gm_adamw_begin(ctypes.byref(prm), state.step.data_ptr(), flag,
-                                      state.scratch.data_ptr(), s), "gm_adamw_begin")
-            for kind, rows in kinds.items():
-                table = _rows(*zip(*rows))
-                _check(lib.gm_adamw_apply(len(rows), table, *kind, ctypes.byref(prm),
-                                          state.scratch.data_ptr(), s), "gm_adamw_apply")
+            else:
+                kinds = [_DT[t.dtype] for ts in zip(params, grads, copies or params) for t in ts]
+                _check(lib.gm_adamw_step_mixed(n, table, struct.pack(f"{3 * n}i", *kinds), ctypes.byref(prm),
+                                               state.step.data_ptr(), flag, state.scratch.data_ptr(), s),
+                       "gm_adamw_step_mixed")
 
 
 # ------------------------------------------------ microscaled 4-bit operands

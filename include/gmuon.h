@@ -470,10 +470,22 @@ gm_status gm_adamw_step(int count, const gm_adamw_tensor* tensors, gm_dtype pdt,
                         gm_dtype cdt, const gm_adamw_params* params, int64_t* step,
                         const int32_t* skip, void* scratch, gm_stream_t stream);
 /*
- * The same for lists of mixed dtypes, one call per combination: gm_adamw_begin
+ * The same for a list of mixed dtypes: tensors[i] has dtypes[i], at most 65536 tensors
+ * of each combination. The whole list is checked before anything is enqueued.
+ */
+typedef struct {
+  gm_dtype p, g, copy;       /* copy: any where the tensor has none */
+} gm_adamw_dtypes;
+gm_status gm_adamw_step_mixed(int count, const gm_adamw_tensor* tensors,
+                              const gm_adamw_dtypes* dtypes, const gm_adamw_params* params,
+                              int64_t* step, const int32_t* skip, void* scratch,
+                              gm_stream_t stream);
+/*
+ * The step in parts, for lists that come one after the other: gm_adamw_begin
  * once (step count, coefficients into scratch, the skip flag), then
  * gm_adamw_apply for each list with the same params and scratch.
- * gm_adamw_step = gm_adamw_begin, then one gm_adamw_apply.
+ * gm_adamw_step = gm_adamw_begin, then one gm_adamw_apply. A list that
+ * gm_adamw_apply refuses is left out of a step that has been counted.
  */
 gm_status gm_adamw_begin(const gm_adamw_params* params, int64_t* step, const int32_t* skip,
                          void* scratch, gm_stream_t stream);
