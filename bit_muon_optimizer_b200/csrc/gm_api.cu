@@ -3,6 +3,7 @@
 
 #include <stdarg.h>
 #include <atomic>
+#include <algorithm>
 #include <cmath>
 #include <memory>
 #include <new>
@@ -120,6 +121,26 @@ constexpr int kMaxList = 65536;   // tensors of a multi-tensor call
 bool aligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 bool dtype_ok(int dt) { return dt == GM_F32 || dt == GM_BF16 || dt == GM_F16; }
 size_t dtype_bytes(int dt) { return dt == GM_F32 ? 4 : 2; }
+// Memory that a call writes, and memory that it only reads.
+struct Span {
+  uintptr_t lo, hi;
+  bool operator<(const Span& o) const { return lo < o.lo; }
+};
+Span span_of(const void* p, size_t bytes) {
+  return {reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes};
+}
+// No byte is written through two arrays, or written through one and read through
+// another. `written` is sorted in place.
+bool disjoint(Span* written, size_t nw, const Span* read, size_t nr) {
+  std::sort(written, written + nw);
+  for (size_t i = 1; i < nw; ++i)
+    if (written[i].lo < written[i - 1].hi) return false;
+  for (size_t i = 0; i < nr; ++i) {
+    const Span* w = std::upper_bound(written, written + nw, read[i]);   // the first behind read[i].lo
+    if ((w != written + nw && w->lo < read[i].hi) || (w != written && w[-1].hi > read[i].lo)) return false;
+  }
+  return true;
+}
 bool mx4_shape_ok(int B, int rows, int cols) {
   return B >= 1 && B <= 65535 && rows >= 1 && rows <= (1 << 24) && cols >= 1 && cols <= (1 << 24) &&
          (long long)rows * cols <= (1LL << 40);
@@ -789,14 +810,34 @@ static gm_status adamw_tensor_check(int i, const gm_adamw_tensor& x, const gm_ad
   return GM_OK;
 }
 
-static gm_status adamw_list_check(int count, const gm_adamw_tensor* t, gm_dtype pdt, gm_dtype gdt,
-                                  gm_dtype cdt, int bits) {
-  GM_CHECK_ARG(count >= 1 && count <= kMaxList, "count=%d out of [1, %d]", count, kMaxList);
-  GM_CHECK_ARG(t, "NULL list");
+// `dtypes`: one of each tensor, or (stride 0) the same of all.
+static gm_status adamw_list_check(int count, const gm_adamw_tensor* t, const gm_adamw_dtypes* dtypes, int stride,
+                                  int bits) {
   for (int i = 0; i < count; ++i) {
-    const gm_status chk = adamw_tensor_check(i, t[i], {pdt, gdt, cdt}, bits);
+    const gm_status chk = adamw_tensor_check(i, t[i], dtypes[i * stride], bits);
     if (chk != GM_OK) return chk;
   }
+  const int per = bits == 32 ? 4 : 6;
+  const std::unique_ptr<Span[]> spans(new (std::nothrow) Span[(size_t)count * (per + 1)]);
+  if (!spans) return set_error(GM_E_WORKSPACE, "no host memory for a list of %d tensors", count);
+  Span *w = spans.get(), *g = spans.get() + (size_t)count * per;
+  for (int i = 0; i < count; ++i) {
+    const gm_adamw_tensor& x = t[i];
+    const gm_adamw_dtypes& dt = dtypes[i * stride];
+    const size_t n = (size_t)x.numel, state = bits == 32 ? 4 * n : n;
+    *w++ = span_of(x.p, n * dtype_bytes(dt.p));
+    // a copy of the parameter's type may be the parameter itself
+    if (x.copy && !(x.copy == x.p && dt.copy == dt.p)) *w++ = span_of(x.copy, n * dtype_bytes(dt.copy));
+    *w++ = span_of(x.m, state);
+    *w++ = span_of(x.v, state);
+    if (bits == 8) {
+      *w++ = span_of(x.mscale, (n + 127) / 128 * 4);
+      *w++ = span_of(x.vscale, (n + 127) / 128 * 4);
+    }
+    g[i] = span_of(x.g, n * dtype_bytes(dt.g));
+  }
+  GM_CHECK_ARG(disjoint(spans.get(), w - spans.get(), g, count),
+               "an array that the step writes overlaps another one of the list");
   return GM_OK;
 }
 
@@ -816,7 +857,10 @@ gm_status gm_adamw_apply(int count, const gm_adamw_tensor* tensors, gm_dtype pdt
                          gm_stream_t stream) {
   gm_status chk = adamw_params_check(params);
   if (chk != GM_OK) return chk;
-  chk = adamw_list_check(count, tensors, pdt, gdt, cdt, params->bits);
+  GM_CHECK_ARG(count >= 1 && count <= kMaxList, "count=%d out of [1, %d]", count, kMaxList);
+  GM_CHECK_ARG(tensors, "NULL list");
+  const gm_adamw_dtypes dt{pdt, gdt, cdt};
+  chk = adamw_list_check(count, tensors, &dt, 0, params->bits);
   if (chk != GM_OK) return chk;
   GM_CHECK_ARG(scratch && al16(scratch), "NULL or misaligned scratch");
   GM_DEVICE();
@@ -830,11 +874,16 @@ gm_status gm_adamw_step(int count, const gm_adamw_tensor* tensors, gm_dtype pdt,
                         const int32_t* skip, void* scratch, gm_stream_t stream) {
   gm_status chk = adamw_params_check(params);
   if (chk != GM_OK) return chk;
-  chk = adamw_list_check(count, tensors, pdt, gdt, cdt, params->bits);   // before anything is enqueued
+  GM_CHECK_ARG(count >= 1 && count <= kMaxList, "count=%d out of [1, %d]", count, kMaxList);
+  GM_CHECK_ARG(tensors, "NULL list");
+  const gm_adamw_dtypes dt{pdt, gdt, cdt};
+  chk = adamw_list_check(count, tensors, &dt, 0, params->bits);   // before anything is enqueued
   if (chk != GM_OK) return chk;
   chk = gm_adamw_begin(params, step, skip, scratch, stream);
   if (chk != GM_OK) return chk;
-  return gm_adamw_apply(count, tensors, pdt, gdt, cdt, params, scratch, stream);
+  GM_CUDA(launch_adamw(count, tensors, (int)pdt, (int)gdt, (int)cdt, *params, scratch,
+                       reinterpret_cast<cudaStream_t>(stream)));
+  return GM_OK;
 }
 
 gm_status gm_adamw_step_mixed(int count, const gm_adamw_tensor* tensors, const gm_adamw_dtypes* dtypes,
@@ -844,20 +893,21 @@ gm_status gm_adamw_step_mixed(int count, const gm_adamw_tensor* tensors, const g
   if (chk != GM_OK) return chk;
   GM_CHECK_ARG(count >= 1 && count <= 27 * kMaxList, "count=%d out of [1, %d]", count, 27 * kMaxList);
   GM_CHECK_ARG(tensors && dtypes, "NULL list");
-  for (int i = 0; i < count; ++i) {   // every list before anything is enqueued
-    chk = adamw_tensor_check(i, tensors[i], dtypes[i], params->bits);
-    if (chk != GM_OK) return chk;
+  int first[28] = {0}, at[27];   // of each combination of types in the list below
+  for (int i = 0; i < count; ++i) {
+    const gm_adamw_dtypes& dt = dtypes[i];
+    GM_CHECK_ARG(dtype_ok(dt.p) && dtype_ok(dt.g) && dtype_ok(dt.copy), "bad dtype of tensor %d", i);
+    ++first[dt.p * 9 + dt.g * 3 + dt.copy + 1];
   }
-  // the tensors of each combination of types together, in their order
-  const std::unique_ptr<gm_adamw_tensor[]> list(new (std::nothrow) gm_adamw_tensor[count]);
-  if (!list) return set_error(GM_E_WORKSPACE, "no host memory for a list of %d tensors", count);
-  int first[28] = {0}, at[27];
-  for (int i = 0; i < count; ++i) ++first[dtypes[i].p * 9 + dtypes[i].g * 3 + dtypes[i].copy + 1];
   for (int k = 0; k < 27; ++k) {
     GM_CHECK_ARG(first[k + 1] <= kMaxList, "%d tensors of one combination of types, at most %d", first[k + 1],
                  kMaxList);
     at[k] = first[k + 1] += first[k];
   }
+  chk = adamw_list_check(count, tensors, dtypes, 1, params->bits);   // before anything is enqueued
+  if (chk != GM_OK) return chk;
+  const std::unique_ptr<gm_adamw_tensor[]> list(new (std::nothrow) gm_adamw_tensor[count]);
+  if (!list) return set_error(GM_E_WORKSPACE, "no host memory for a list of %d tensors", count);
   for (int i = count - 1; i >= 0; --i) list[--at[dtypes[i].p * 9 + dtypes[i].g * 3 + dtypes[i].copy]] = tensors[i];
   chk = gm_adamw_begin(params, step, skip, scratch, stream);
   if (chk != GM_OK) return chk;
@@ -879,6 +929,20 @@ gm_status gm_adamw_unpack8(int count, const gm_adamw_state8* tensors, gm_stream_
                      aligned(x.v_out, 4),
                  "a misaligned array of tensor %d", i);
   }
+  const std::unique_ptr<Span[]> spans(new (std::nothrow) Span[(size_t)count * 6]);
+  if (!spans) return set_error(GM_E_WORKSPACE, "no host memory for a list of %d tensors", count);
+  Span *w = spans.get(), *r = spans.get() + (size_t)count * 2;
+  for (int i = 0; i < count; ++i) {
+    const gm_adamw_state8& x = tensors[i];
+    const size_t n = (size_t)x.numel, scales = (n + 127) / 128 * 4;
+    w[2 * i] = span_of(x.m_out, 4 * n);
+    w[2 * i + 1] = span_of(x.v_out, 4 * n);
+    r[4 * i] = span_of(x.m, n);
+    r[4 * i + 1] = span_of(x.v, n);
+    r[4 * i + 2] = span_of(x.mscale, scales);
+    r[4 * i + 3] = span_of(x.vscale, scales);
+  }
+  GM_CHECK_ARG(disjoint(w, (size_t)count * 2, r, (size_t)count * 4), "an output overlaps another array of the list");
   GM_DEVICE();
   GM_CUDA(launch_adamw_unpack8(count, tensors, reinterpret_cast<cudaStream_t>(stream)));
   return GM_OK;

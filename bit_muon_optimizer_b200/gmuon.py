@@ -928,7 +928,9 @@ class AdamWStep:
         ``clip``: a ``grad_norm`` result, whose factor scales the gradients and whose
         status makes the call change nothing; ``skip``: such a flag (int32 [1]) alone;
         ``lr``: this step's rate instead of the object's, a number or an fp32 [1]
-        tensor on the device (read when the step runs, for captured graphs)."""
+        tensor on the device (read when the step runs, for captured graphs). A tensor that
+        is written may overlap no other one of the lists (but ``copies[i]`` may be
+        ``params[i]`` of the same dtype)."""
         dev, numels, pk = _list_of(params, "params", _FLOATS)
         _, _, gk = _list_of(grads, "grads", _FLOATS, dev, numels)
         state.check(numels, dev)
@@ -952,13 +954,6 @@ class AdamWStep:
                    _addresses(state.mscale) if state.bits == 8 else none,
                    _addresses(state.vscale) if state.bits == 8 else none,
                    _addresses(copies) if copies is not None else none, numels]
-        if len(set(columns[0])) != n or len(set(columns[2])) != n:
-            raise ValueError("params: a tensor is in the list more than once")
-        kept = [a for column in columns[2:6 if state.bits == 8 else 4] for a in column]
-        if len(set(kept)) != len(kept):
-            raise ValueError("state: a tensor is in the state more than once")
-        if copies is not None and len(set(columns[6])) != n:
-            raise ValueError("copies: a tensor is in the list more than once")
         prm = AdamWParams(self.lr if lr is None else float(lr), *self.betas, self.eps, self.wd,
                           state.bits, clip.scale.data_ptr() if clip is not None else None, lr_dev)
         flag = skip.data_ptr() if skip is not None else None
@@ -966,14 +961,24 @@ class AdamWStep:
         with _on(dev):
             s = _stream_of(dev)
             if len(pk) == len(gk) == len(ck) == 1:
-                _check(lib.gm_adamw_step(n, table, *[_DT[next(iter(k))] for k in (pk, gk, ck)],
-                                         ctypes.byref(prm), state.step.data_ptr(), flag,
-                                         state.scratch.data_ptr(), s), "gm_adamw_step")
+                status = lib.gm_adamw_step(n, table, *[_DT[next(iter(k))] for k in (pk, gk, ck)],
+                                           ctypes.byref(prm), state.step.data_ptr(), flag,
+                                           state.scratch.data_ptr(), s)
             else:
                 kinds = [_DT[t.dtype] for ts in zip(params, grads, copies or params) for t in ts]
-                _check(lib.gm_adamw_step_mixed(n, table, struct.pack(f"{3 * n}i", *kinds), ctypes.byref(prm),
-                                               state.step.data_ptr(), flag, state.scratch.data_ptr(), s),
-                       "gm_adamw_step_mixed")
+                status = lib.gm_adamw_step_mixed(n, table, struct.pack(f"{3 * n}i", *kinds), ctypes.byref(prm),
+                                                 state.step.data_ptr(), flag, state.scratch.data_ptr(), s)
+            if status != GM_OK:
+                _repeated(columns, state.bits)
+                _check(status, "gm_adamw_step")
+
+
+def _repeated(columns, bits):
+    """Names the list of a step that the library refused where a tensor is in it twice."""
+    kept = [a for column in columns[2:6 if bits == 8 else 4] for a in column]
+    for name, what in (("params", columns[0]), ("state", kept), ("copies", [a for a in columns[6] if a])):
+        if len(set(what)) != len(what):
+            raise ValueError(f"{name}: a tensor is in it more than once")
 
 
 # ------------------------------------------------ microscaled 4-bit operands

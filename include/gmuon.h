@@ -439,7 +439,9 @@ gm_status gm_grad_norm(int count, const gm_grad* grads, double max_norm, float* 
  *     whole; an infinity (for v: a sum past fp32's range) leaves an infinite scale,
  *     under which m is NaN and v infinite. Each moment by itself: a v past fp32's
  *     range leaves an m that is not as defined above.
- *     No two entries may overlap. All-zero codes and scales are the zero state.
+ *     What is written (p, copy, m, v, the scales) may not overlap anything else in the
+ *     list, but a copy of p's type may be p itself; gradients may be shared. An overlap
+ *     is refused. All-zero codes and scales are the zero state.
  *   step int64 [1] (device): completed steps, incremented by this one; scratch:
  *   GM_ADAMW_SCRATCH_BYTES of device memory, 16-byte aligned, that belong to this
  *   step count (calls that overlap on the GPU need their own).
@@ -493,7 +495,8 @@ gm_status gm_adamw_apply(int count, const gm_adamw_tensor* tensors, gm_dtype pdt
                          gm_dtype cdt, const gm_adamw_params* params, const void* scratch,
                          gm_stream_t stream);
 
-/* fp32 m and v of 8-bit AdamW states (layouts and rules as in gm_adamw_step). */
+/* fp32 m and v of 8-bit AdamW states (layouts and rules as in gm_adamw_step; outputs
+ * overlap nothing). */
 typedef struct {
   const uint8_t* m;
   const uint8_t* v;
