@@ -141,6 +141,18 @@ bool disjoint(Span* written, size_t nw, const Span* read, size_t nr) {
   }
   return true;
 }
+// Does the span hold a byte of B x m rows of `row` bytes? (Outputs may lie in the gaps of
+// a strided matrix.)
+bool meets_rows(const Span& w, const void* X, int B, int m, size_t row, size_t row_stride, size_t batch_stride) {
+  for (int b = 0; b < B; ++b) {
+    const uintptr_t base = reinterpret_cast<uintptr_t>(X) + b * batch_stride;
+    if (w.hi <= base || w.lo >= base + (m - 1) * row_stride + row) continue;
+    const size_t r = w.lo <= base || m == 1 ? 0 : (w.lo - base) / row_stride;
+    const uintptr_t at = base + r * row_stride;   // the last row that begins at or before w.lo, or the first
+    if (w.lo < at + row || (r + 1 < (size_t)m && w.hi > at + row_stride)) return true;
+  }
+  return false;
+}
 bool mx4_shape_ok(int B, int rows, int cols) {
   return B >= 1 && B <= 65535 && rows >= 1 && rows <= (1 << 24) && cols >= 1 && cols <= (1 << 24) &&
          (long long)rows * cols <= (1LL << 40);
@@ -716,6 +728,24 @@ gm_status gm_mx4_quant(int B, int m, int n, const void* X, gm_dtype xdt, int64_t
   GM_CHECK_ARG(al16(codes) && al16(scales) && al16(codesT) && al16(scalesT),
                "device arrays must be 16-byte aligned");
   GM_CHECK_ARG(fmt == GM_MX4 || (gscale && aligned(gscale, 4)), "GM_NV4 needs gscale");
+  {
+    Span w[5];
+    size_t nw = 0;
+    if (codes) {
+      w[nw++] = span_of(codes, gm_mx4_codes_bytes(B, m, n));
+      w[nw++] = span_of(scales, gm_mx4_scales_bytes(B, m, n, fmt));
+    }
+    if (codesT) {
+      w[nw++] = span_of(codesT, gm_mx4_codes_bytes(B, n, m));
+      w[nw++] = span_of(scalesT, gm_mx4_scales_bytes(B, n, m, fmt));
+    }
+    if (fmt == GM_NV4) w[nw++] = span_of(gscale, (size_t)B * 4);
+    bool apart = disjoint(w, nw, nullptr, 0);
+    const size_t es = dtype_bytes(xdt);
+    for (size_t i = 0; i < nw; ++i)
+      apart = apart && !meets_rows(w[i], X, batch_stride ? B : 1, m, n * es, row_stride * es, batch_stride * es);
+    GM_CHECK_ARG(apart, "an output overlaps X or another output");
+  }
   GM_DEVICE();
   GM_CUDA(launch_mx4_quant(B, m, n, X, (int)xdt, row_stride, batch_stride, (int)fmt, gscale, codes,
                            scales, codesT, scalesT, reinterpret_cast<cudaStream_t>(stream)));
@@ -730,6 +760,12 @@ gm_status gm_mx4_dequant(int B, int rows, int cols, gm_mx4_format fmt, const uin
   GM_CHECK_ARG(codes && scales && X_out, "NULL pointer");
   GM_CHECK_ARG(al16(codes) && al16(scales) && al16(X_out), "device arrays must be 16-byte aligned");
   GM_CHECK_ARG(fmt == GM_MX4 || (gscale && aligned(gscale, 4)), "GM_NV4 needs gscale");
+  {
+    Span w = span_of(X_out, (size_t)B * rows * cols * dtype_bytes(odt));
+    const Span r[3] = {span_of(codes, gm_mx4_codes_bytes(B, rows, cols)),
+                       span_of(scales, gm_mx4_scales_bytes(B, rows, cols, fmt)), span_of(gscale, (size_t)B * 4)};
+    GM_CHECK_ARG(disjoint(&w, 1, r, fmt == GM_NV4 ? 3 : 2), "X_out overlaps the operand");
+  }
   GM_DEVICE();
   GM_CUDA(launch_mx4_dequant(B, rows, cols, (int)fmt, codes, scales, gscale, X_out, (int)odt,
                              reinterpret_cast<cudaStream_t>(stream)));
@@ -749,6 +785,13 @@ gm_status gm_mx4_matmul(int B, int M, int N, int K, gm_mx4_format fmt, const uin
                "device arrays must be 16-byte aligned");
   GM_CHECK_ARG(fmt == GM_MX4 || (A_gscale && B_gscale && aligned(A_gscale, 4) && aligned(B_gscale, 4)),
                "GM_NV4 needs both gscale");
+  {
+    Span w = span_of(D, (size_t)B * M * N * dtype_bytes(ddt));
+    const Span r[6] = {span_of(A_codes, gm_mx4_codes_bytes(B, M, K)), span_of(A_scales, gm_mx4_scales_bytes(B, M, K, fmt)),
+                       span_of(B_codes, gm_mx4_codes_bytes(B, N, K)), span_of(B_scales, gm_mx4_scales_bytes(B, N, K, fmt)),
+                       span_of(A_gscale, (size_t)B * 4), span_of(B_gscale, (size_t)B * 4)};
+    GM_CHECK_ARG(disjoint(&w, 1, r, fmt == GM_NV4 ? 6 : 4), "D overlaps an operand");
+  }
   GM_DEVICE();
   GM_CUDA(launch_mx4_matmul(B, M, N, K, (int)fmt, A_codes, A_scales, A_gscale, B_codes, B_scales,
                             B_gscale, D, (int)ddt, accumulate,

@@ -543,14 +543,15 @@ size_t gm_mx4_scales_bytes(int B, int rows, int cols, gm_mx4_format fmt);
  *   X of dtype xdt, element (b, i, j) at X[b * batch_stride + i * row_stride + j]
  *   (strides in elements, non-negative, row_stride >= n unless m = 1); element
  *   alignment suffices (rows that do not start on 16 bytes are read element by
- *   element).
+ *   element). Outputs overlap neither X nor one another.
  */
 gm_status gm_mx4_quant(int B, int m, int n, const void* X, gm_dtype xdt, int64_t row_stride,
                        int64_t batch_stride, gm_mx4_format fmt, float* gscale, uint8_t* codes,
                        uint8_t* scales, uint8_t* codesT, uint8_t* scalesT, gm_stream_t stream);
 
 /* What an operand stands for: X_out [B][rows][cols] of dtype odt (the product of
- * the two or three factors in fp32, rounded once to odt). */
+ * the two or three factors in fp32, rounded once to odt); it does not overlap the
+ * operand. */
 gm_status gm_mx4_dequant(int B, int rows, int cols, gm_mx4_format fmt, const uint8_t* codes,
                          const uint8_t* scales, const float* gscale, void* X_out, gm_dtype odt,
                          gm_stream_t stream);
@@ -558,8 +559,9 @@ gm_status gm_mx4_dequant(int B, int rows, int cols, gm_mx4_format fmt, const uin
 /*
  * D[b] = A[b] Bm[b]^T (+ D[b] with accumulate = 1): A an M x K operand, Bm an N x K
  * operand of the same format, D [B][M][N] of dtype ddt (16-byte aligned); sums in
- * fp32 in a fixed order, one rounding. A NaN scale makes its row (A) or column (Bm)
- * NaN. No workspace. A wait that runs out is reported by gm_device_errors().
+ * fp32 in a fixed order, one rounding. D overlaps no operand. A NaN scale makes its row
+ * (A) or column (Bm) NaN. No workspace. A wait that runs out is reported by
+ * gm_device_errors().
  */
 gm_status gm_mx4_matmul(int B, int M, int N, int K, gm_mx4_format fmt, const uint8_t* A_codes,
                         const uint8_t* A_scales, const float* A_gscale, const uint8_t* B_codes,
