@@ -1002,20 +1002,23 @@ class Mx4:
     codes: torch.Tensor
     scales: torch.Tensor
     gscale: torch.Tensor | None = None
+    paired: bool = field(default=False, repr=False, compare=False)   # gscale is its transpose's too
 
     @staticmethod
     def empty(B, rows, cols, fmt, device=None, gscale=None):
-        """An operand's buffers; ``gscale`` to share another operand's (its transpose's)."""
+        """An operand's buffers; ``gscale`` to share another operand's (its transpose's):
+        the two are then one pair, to be written together."""
         if fmt not in MX4_BLOCK:
             raise ValueError(f"fmt: GM_MX4 or GM_NV4 expected, got {fmt}")
         dev = device or torch.device("cuda")
         kp = _mx4_padded(cols)
+        paired = fmt == GM_NV4 and gscale is not None
         if fmt == GM_NV4 and gscale is None:
             gscale = torch.empty(B, dtype=torch.float32, device=dev)
         return Mx4(fmt, rows, cols,
                    torch.empty((B, rows, kp // 2), dtype=torch.uint8, device=dev),
                    torch.empty((B, -(-rows // 128), kp // (4 * MX4_BLOCK[fmt]), 32, 4, 4),
-                               dtype=torch.uint8, device=dev), gscale)
+                               dtype=torch.uint8, device=dev), gscale, paired)
 
     def tensors(self):
         return [self.codes, self.scales] + ([self.gscale] if self.gscale is not None else [])
@@ -1063,7 +1066,9 @@ def mx4_quant(X, fmt=GM_MX4, rows=True, cols=False, out=None):
     """Microscaled 4-bit operands of X [B, m, n] (or [m, n]; fp32, bf16 or fp16; rows of
     any stride, neighbouring elements of a row adjacent): of X itself (``rows``), of its
     transpose (``cols``, quantised along X's columns), or both from one pass, as a pair.
-    ``out``: the operand (or pair) to write into."""
+    The operands of a GM_NV4 pair share one ``gscale``. ``out``: the operand (or pair) to
+    write into; an operand of a GM_NV4 pair is written together with the other one only,
+    which would else stand for its old codes under the new matrix's scale."""
     B, m, n = _bmn(X)
     if X.dtype not in _DT:
         raise ValueError(f"X: dtype {X.dtype} is not one of {tuple(_DT)}")
@@ -1086,13 +1091,19 @@ def mx4_quant(X, fmt=GM_MX4, rows=True, cols=False, out=None):
                 continue
             if (o.fmt, o.rows, o.cols) != (fmt, r, c) or o.check(name) != B or o.codes.device != dev:
                 raise ValueError(f"{name}: expected {B} operands of {r} x {c} in format {fmt} on {dev}")
-        if q is not None and qt is not None and fmt == GM_NV4 and q.gscale.data_ptr() != qt.gscale.data_ptr():
-            raise ValueError("out: the two operands of one matrix share one gscale")
+        if q is not None and qt is not None:
+            if fmt == GM_NV4 and q.gscale.data_ptr() != qt.gscale.data_ptr():
+                raise ValueError("out: the two operands of one matrix share one gscale")
+        elif (q or qt).paired:
+            raise ValueError("out: one of a pair, whose other operand shares its gscale: write the pair, or an "
+                             "operand of its own (Mx4.empty)")
     else:
         if rows:
             q = Mx4.empty(B, m, n, fmt, dev)
         if cols:
             qt = Mx4.empty(B, n, m, fmt, dev, gscale=q.gscale if rows else None)
+    if rows and cols and fmt == GM_NV4:
+        q.paired = qt.paired = True
     gs = (q or qt).gscale
     with _on(dev):
         _check(lib.gm_mx4_quant(B, m, n, X.data_ptr(), _DT[X.dtype], X.stride(-2) if m > 1 else n,
