@@ -199,14 +199,14 @@ __device__ __forceinline__ uint32_t group_max(uint32_t x) {
 // --------------------------------------------------------------------- the step
 // What every chunk of a step needs, computed once per step by k_adamw_begin.
 struct Coef {
-  double c;          // clip factor (1 without)
-  float c1, c2;      // c = c1 c2 in fp32, c2 = 1 unless c is no normal fp32 number
+  double c;          // clip factor (1 without) over c1
+  float c32;
+  float c1;          // 1, or a power of two that gradients take first (see k_adamw_begin)
   float decay;       // 1 - lr wd
   float scale;       // lr / (1 - b1^t)
   float root;        // 1 / sqrt(1 - b2^t)
   float root8, eps8; // root / scale, eps / scale: the update is m / (r root8 + eps8)
   int skip;
-  int wide;          // c times 1 - b1 or the root of 1 - b2 is no normal fp32 number
 };
 static_assert(sizeof(Coef) <= GM_ADAMW_SCRATCH_BYTES, "the step's scratch holds the coefficients");
 
@@ -220,14 +220,15 @@ __global__ void k_adamw_begin(double lr, double b1, double b2, double eps, doubl
   const long long t = *step + 1;
   *step = t;
   const double l = lr_dev ? (double)*lr_dev : lr;
-  const double c = clip ? *clip : 1.0;
-  out->c = c;
-  // What fp32 cannot hold of c: a power of two first, which is exact where it matters.
-  const bool low = fabs(c) < pow2d(-126), high = fabs(c) > pow2d(127);
-  const double c1 = low ? pow2d(-126) : high ? pow2d(126) : c;
+  // A clip factor that, alone or times 1 - b1 or the root of 1 - b2, is no normal fp32
+  // number (a norm near fp32's end gives one): gradients take a power of two first, which
+  // leaves a factor that is. It is exact but for products that fp32 cannot hold either.
+  const double c = clip ? *clip : 1.0, a = fabs(c);
+  const bool low = c != 0.0 && a * fmin(1.0 - b1, sqrt(1.0 - b2)) < pow2d(-126);
+  const double c1 = a > pow2d(127) ? pow2d(126) : low ? pow2d(a < pow2d(-150) ? -126 : -64) : 1.0;
+  out->c = c / c1;
+  out->c32 = (float)(c / c1);
   out->c1 = (float)c1;
-  out->c2 = low || high ? (float)fmin(fmax(c / c1, -3e38), 3e38) : 1.f;
-  out->wide = high || (c != 0.0 && !(fabs(c) * fmin(1.0 - b1, sqrt(1.0 - b2)) >= pow2d(-126)));
   out->decay = (float)(1.0 - l * wd);
   const double s = l / (1.0 - pow(b1, (double)t)), r = 1.0 / sqrt(1.0 - pow(b2, (double)t));
   out->scale = (float)s;
@@ -276,7 +277,7 @@ struct Codes8 {
 struct Eight {
   float x[8];
 };
-__device__ __noinline__ Codes8 exact_codes(const Consts& k, double c, Eight g, uint2 mc, uint2 vc, float ms, float vs) {
+__device__ __noinline__ Codes8 exact_codes(const Consts k, double c, Eight g, uint2 mc, uint2 vc, float ms, float vs) {
   float mo[8], ml[4], mh[4];
   e4m3x4_to_float(mc.x, ml);
   e4m3x4_to_float(mc.y, mh);
@@ -316,23 +317,25 @@ __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, u
 }
 
 // Eight elements a lane, element i the first. WHOLE: the warp's part lies inside the
-// tensor, whose arrays are aligned to eight elements. WIDE (8 bits): for clip factors that
-// fp32 cannot hold (a norm near fp32's end gives them): gradients times the factor in
-// fp64, and all codes from fp64.
-template <int PDT, int GDT, int BITS, bool WHOLE, bool WIDE>
+// tensor, whose arrays are aligned to eight elements.
+template <int PDT, int GDT, int BITS, bool WHOLE>
 __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const Coef* coef, const Coef& f,
                                           long long i, int lane) {
   const long long n = E.numel - i;
   float p[8], g[8];
   load8<PDT, WHOLE>(E.p, i, n, p);
   load8<GDT, WHOLE>(E.g, i, n, g);
+  if (f.c1 != 1.f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] *= f.c1;
+  }
   if constexpr (BITS == 32) {
     float m[8], v[8];
     load8<GM_F32, WHOLE>(E.m, i, n, m);
     load8<GM_F32, WHOLE>(E.v, i, n, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float gc = g[e] * f.c1 * f.c2;
+      const float gc = g[e] * f.c32;
       m[e] = fmaf(k.b1, m[e], k.ob1 * gc);
       // in this order: g^2 alone leaves fp32's range before (1 - b2) g^2 does
       v[e] = fmaf(k.ob2 * gc, gc, k.b2 * v[e]);
@@ -352,7 +355,7 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
     // b1 sm and the roots of b2 and 1 - b2 go into the group's factors:
     // m' = code (b1 sm) + g (1 - b1) c, v' = (root sv sqrt(b2))^2 + (g c sqrt(1 - b2))^2
     const float ma = k.b1 * ms, va = k.rb2 * vs;
-    const float cm = WIDE ? k.ob1 : k.ob1 * f.c1, cv = WIDE ? k.rob2 : k.rob2 * f.c1;
+    const float cm = k.ob1 * f.c32, cv = k.rob2 * f.c32;
     float m[8], size[8], r[8];
     uint32_t vb[8];
     {
@@ -366,9 +369,8 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
     uint32_t tvb = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float gc = WIDE ? (float)((double)g[e] * f.c) : g[e];
-      const float a = m[e] * ma, b = gc * cm;
-      const float r0 = root_value((e < 4 ? vc.x : vc.y) >> (8 * (e & 3)) & 255u) * va, g0 = gc * cv;
+      const float a = m[e] * ma, b = g[e] * cm;
+      const float r0 = root_value((e < 4 ? vc.x : vc.y) >> (8 * (e & 3)) & 255u) * va, g0 = g[e] * cv;
       size[e] = fabsf(a) + fabsf(b);
       m[e] = a + b;
       float v = fmaf(r0, r0, g0 * g0);
@@ -404,7 +406,7 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
     // Near fp32's subnormals these bounds do not hold: 2^-90 and 2^-80 keep the
     // smallest element that gets a code (2^-18 of the top) and its square above them,
     // and 2^14 keeps 1 / sv 2^112 below.
-    bool near = WIDE || ts > 3.f * tm;
+    bool near = f.c1 != 1.f || ts > 3.f * tm;   // (the scales below read gradients again)
     if (tm < 8.1e-28f || tv < 8.3e-25f || sv > 16384.f) near |= ts > 0.f || tvb > 0;
     const float im = approx_rcp(sm), iv = approx_rcp(sv) * 1.925929944387236e-34f;   // 2^-112
     const float w = im * 1.66893005e-6f;   // 28 u
@@ -454,15 +456,17 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
       const uint32_t om = __ballot_sync(0xffffffffu, gm ? tmb + kTie >= gm : lane == first);
       const uint32_t ov = __ballot_sync(0xffffffffu, gv ? tvb + kTie >= gv : lane == first);
       const bool of_v = (lane & 8) != 0;
-      const uint8_t* codes = static_cast<const uint8_t*>(of_v ? E.v : E.m);
       const double scale = (double)(of_v ? vs : ms);
       uint32_t todo = (of_v ? ov : om) >> first & 0xFFFFu;
       const long long group0 = i - (lane & 15) * 8 + (lane & 7);
       double d = 0.0;
       do {
         const long long at = group0 + (__ffs(todo) - 1) * 8;
+        const int src = first + max(__ffs(todo) - 1, 0);
+        const uint32_t mx = __shfl_sync(0xffffffffu, mc.x, src), my = __shfl_sync(0xffffffffu, mc.y, src);
+        const uint32_t vx = __shfl_sync(0xffffffffu, vc.x, src), vy = __shfl_sync(0xffffffffu, vc.y, src);
         if (todo && (WHOLE || at < E.numel)) {
-          const uint32_t code = codes[at];
+          const uint32_t code = (of_v ? (lane & 4 ? vy : vx) : (lane & 4 ? my : mx)) >> (8 * (lane & 3)) & 255u;
           double x = (double)(of_v ? root_value(code) : e4m3_value(code)) * scale;
           double y = __dmul_rn((double)one<GDT>(E.g, at), coef->c);
           if (of_v) {
@@ -492,42 +496,27 @@ __device__ __forceinline__ void step_part(const Entry& E, const Consts& k, const
   }
 }
 
-template <int PDT, int GDT, int BITS, bool WIDE, int N>
-__device__ __forceinline__ void walk(const Table<N>& t, const Consts& k, const Coef* coef, const Coef& f) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int ti = 0;
-  for (int chunk = blockIdx.x; chunk < t.map.total(); chunk += gridDim.x) {
-    ti = t.map.find(chunk, ti);
-    const Entry& E = t.e[ti];
-    const long long base = (long long)(chunk - t.map.first[ti]) * kChunk + warp * kPart;
-    if (!WIDE && t.vec[ti] && base + kPart <= E.numel)
-      step_part<PDT, GDT, BITS, true, WIDE>(E, k, coef, f, base + lane * 8, lane);
-    else if (base < E.numel)
-      step_part<PDT, GDT, BITS, false, WIDE>(E, k, coef, f, base + lane * 8, lane);
-  }
-}
-// Out of line: no ordinary step comes here.
-template <int PDT, int GDT, int N>
-__device__ __noinline__ void walk_wide8(const Table<N>& t, const Consts k, const Coef* coef) {
-  const Coef f = *coef;
-  walk<PDT, GDT, 8, true>(t, k, coef, f);
-}
-
+// 32-bit states: 64 registers, for a fourth CTA on each SM (LLaMA-1.1B set 3680 us, 3825
+// with three).
 template <int PDT, int GDT, int BITS, int N>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, BITS == 32 ? 4 : 3)
     k_adamw(const __grid_constant__ Table<N> t, const Consts k, const Coef* coef) {
   // k_adamw_begin may still be writing *coef until here: no __restrict__, which would
   // promise that nothing writes it while this kernel lives
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Coef f = *coef;
   if (f.skip) return;
-  if constexpr (BITS == 8) {
-    if (f.wide) {
-      walk_wide8<PDT, GDT>(t, k, coef);
-      return;
-    }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int ti = 0;
+  for (int chunk = blockIdx.x; chunk < t.map.total(); chunk += gridDim.x) {
+    ti = t.map.find(chunk, ti);
+    const Entry& E = t.e[ti];
+    const long long base = (long long)(chunk - t.map.first[ti]) * kChunk + warp * kPart;
+    if (t.vec[ti] && base + kPart <= E.numel)
+      step_part<PDT, GDT, BITS, true>(E, k, coef, f, base + lane * 8, lane);
+    else if (base < E.numel)
+      step_part<PDT, GDT, BITS, false>(E, k, coef, f, base + lane * 8, lane);
   }
-  walk<PDT, GDT, BITS, false>(t, k, coef, f);
 }
 
 // ------------------------------------------------------ 8-bit states to fp32
