@@ -10,9 +10,9 @@
 // states and a 16-bit gradient; one pass moves each byte once. The tensor table travels
 // in the kernel's parameters, so a list of any addresses needs no copy to the device
 // and can be captured into a graph. Measured on 1e8 elements with a bf16 gradient and a
-// bf16 copy: 32-bit states 410 us (6.8 TB/s: HBM); 8-bit states 380 us (4.2 TB/s),
-// bound by issue: 83 instructions an element, 63 % of the issue slots (scales rounded
-// from fp64, without which the states would drift from their definition, cost 45 us).
+// bf16 copy: 32-bit states 412 us (6.8 TB/s: HBM); 8-bit states 374 us (4.3 TB/s),
+// bound by issue: 88 instructions an element, 64 % of the issue slots (scales rounded
+// from fp64, without which the states would drift from their definition, cost 51 us).
 
 #include <math.h>
 
@@ -580,7 +580,9 @@ struct GradEntry {
 };
 constexpr int kMaxGrads = 1024, kFewGrads = 64;
 // Elements of a chunk, and CTAs (and partial sums) of a launch: 4e8 bf16 elements take
-// 126 us (6.4 TB/s), 143 us with half the chunk and two thirds of the CTAs.
+// 126 us (6.4 TB/s), 143 us with half the chunk and two thirds of the CTAs. A constant,
+// six for each of a B200's SMs: the workspace's size and the order of the sums do not
+// change with the device that is current.
 constexpr int kNormChunk = 32768;
 constexpr int kNormBlocks = 6 * 148;
 template <int N>
@@ -733,8 +735,8 @@ cudaError_t adamw_list(int n, const gm_adamw_tensor* tensors, int pdt, int gdt, 
   }
   const int total = t.map.first[n];
   // 32-bit states: a chunk per CTA, whose launch order walks the arrays front to
-  // back (1e8 elements 410 us, 467 us with resident CTAs that stride); 8-bit states:
-  // resident CTAs, which save a CTA's start per chunk (337 us, 416 us).
+  // back (1e8 elements 412 us, 478 us with resident CTAs that stride); 8-bit states:
+  // resident CTAs, which save a CTA's start per chunk (374 us, 405 us).
   const int resident = 3 * sm_count();
   const int grid = bits == 32 || total < resident ? total : resident;
   return launch_after(bits == 32 ? pick<32, N>(pdt, gdt) : pick<8, N>(pdt, gdt), grid, s, t, k,

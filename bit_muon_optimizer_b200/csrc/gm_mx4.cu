@@ -13,8 +13,9 @@
 // that for the matrix scale. What bounds the kernels is issue: 8192 x 8192 bf16 both
 // ways take 18 instructions an element (GM_MX4, 54 us, 3.8 TB/s) or 32 (GM_NV4, 92 us:
 // twice the products and conversions, for each element is coded a little below and a
-// little above its quotient to see whether fp32 decides). 16384 x 8192 bf16, GM_MX4:
-// rows 65 us (5.2 TB/s), both 96 us; 18944 x 3584 fp32, GM_NV4, both: 150 us with its
+// little above its quotient to see whether fp32 decides). 16384 x 8192 bf16: rows
+// 65 us (GM_MX4, 5.2 TB/s) or 107 us and 41 us for the matrix scale (GM_NV4, 3.2 and 6.5
+// TB/s), both ways 96 us (GM_MX4); 18944 x 3584 fp32, GM_NV4, both: 150 us with its
 // matrix scale (two such matrices: 79 us of 290, 6.9 TB/s).
 
 #include <math.h>

@@ -7,7 +7,7 @@
 //   CG = 2: a pair of CTAs per 256 x 256 tile (M = 256, N = 256, K = 64 per
 //     instruction), persistent over the tiles. Each CTA loads its 128 rows of A and
 //     128 of the 256 rows of B. 8192 x 18944 x 3584 into bf16: 237 us (GM_MX4, 4.7
-//     PFLOP/s), 230 us (GM_NV4) at 1.6 GHz; without its stores 174 us,
+//     PFLOP/s), 227 us (GM_NV4) at 1.6 GHz; without its stores 174 us,
 //     with a quarter of its MMAs 196 us, with neither 124 us (36 KB a stage and SM, 68
 //     bytes a clock, is what L2 delivers). So loads, MMAs and stores share the memory
 //     path of an SM: 64 bytes a clock of copies into shared memory, as many of operand
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (FMT == GM_NV4) {
 #pragma unroll
           for (int e = 0; e < 64; ++e) v[e] *= alpha.a;
-          if (alpha.b != 1.f) {   // (without this branch 8192 x 18944 x 3584 takes 237 us, not 226)
+          if (alpha.b != 1.f) {   // (without this branch 8192 x 18944 x 3584 takes 231 us, not 227)
 #pragma unroll
             for (int e = 0; e < 64; ++e) v[e] *= alpha.b;
           }
@@ -669,9 +669,16 @@ cudaError_t launch_mx4_matmul(int B, int M, int N, int K, int fmt, const uint8_t
   p.ag = ag; p.bg = bg;
   p.err = device_error_word();
   if (!p.err) return cudaErrorUnknown;
-  // Pairs from a quarter of the SMs' worth of tiles on (2048 x 2048 x 2048: 64 tiles, 11.7
-  // us); up to 128 rows a tile of one CTA reads the weight as fast (16 x 18944 x 3584: 12.6
-  // us, 15.5 as pairs), and few tiles leave pairs idle (1001 x 2053 x 771: 8.7 us alone).
+  // Pairs from a quarter of the SMs' worth of tiles on; up to 128 rows a tile of one CTA
+  // reads the weight as fast (16 x 18944 x 3584: 12.6 us, 15.5 as pairs). Around the limit
+  // K decides more than the tiles do: short sums are faster alone (by a quarter at most),
+  // long ones as pairs (by a fifth). As pairs / alone, us:
+  //   tiles       K = 512     2048         4096          16384
+  //   36 (NV4)   7.4 / 6.3   9.5 / 9.2    12.3 / 13.4   30.0 / 28.8   (MX4: 11.2 / 8.4, 31.1 / 26.3)
+  //   40 (NV4)   7.7 / 6.3   9.7 / 9.2    12.5 / 13.4   30.8 / 37.3
+  //   48 (NV4)   7.7 / 6.3   9.7 / 9.4    12.5 / 13.5   30.9 / 37.9   (MX4: 11.4 / 8.4, 31.8 / 33.2)
+  //   64 (NV4)   7.7 / 6.5  10.0 / 9.6    12.9 / 13.8   32.0 / 38.7   (MX4: 11.6 / 8.7, 32.9 / 34.2)
+  // (1536 x 1536, 1280 x 2048, 1536 x 2048, 2048 x 2048; a choice by K too is not made.)
   const bool pair = M > 128 && (long long)cdiv(M, 256) * cdiv(N, kBN) * B >= sm_count() / 4;
   p.split = 1;
   Maps m;

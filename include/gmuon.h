@@ -454,7 +454,7 @@ typedef struct {
      that fp32 loses below its numbers then moves an update by less than 1e-4 lr */
   double lr, beta1, beta2, eps, wd;
   int bits;                  /* states: 32 or 8 */
-  const double* clip;        /* device [1], nullable: factor of the gradients */
+  const double* clip;        /* device [1], nullable: factor of the gradients, 2^250 at most */
   const float* lr_dev;       /* device [1], nullable: takes lr's place (a schedule under
                                 a captured graph) */
 } gm_adamw_params;
