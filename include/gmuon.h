@@ -437,8 +437,8 @@ gm_status gm_grad_norm(int count, const gm_grad* grads, double max_norm, float* 
  *     operation above rounded singly (/ 448 and / 1.9375 as products with the
  *     rounded reciprocal). A NaN that enters a group makes its m and v NaN as a
  *     whole; an infinity (for v: a sum past fp32's range) leaves an infinite scale,
- *     under which m is NaN and v infinite. Each moment by itself: a v past fp32's
- *     range leaves an m that is not as defined above.
+ *     under which m is NaN and v infinite. One moment's infinity does not touch the
+ *     other's codes and scale.
  *     What is written (p, copy, m, v, the scales) may not overlap anything else in the
  *     list, but a copy of p's type may be p itself; gradients may be shared. An overlap
  *     is refused. All-zero codes and scales are the zero state.
